@@ -37,6 +37,8 @@ EXPORTS = (
     "dd_denoise_block_adaptive_graph_create", "dd_denoise_block_adaptive_graph_launch",
     "dd_denoise_block_adaptive_graph_destroy", "dd_ffw_workspace", "dd_ffw",
     "dd_self_condition_workspace", "dd_self_condition", "dd_set_test_stall_ns",
+    "dd_cache_workspace", "dd_cache_append", "dd_cache_read", "dd_paged_attn_workspace",
+    "dd_paged_attn", "dd_verify_draft_workspace", "dd_verify_draft",
 )
 
 
@@ -60,6 +62,23 @@ class SampleParams(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("renoise_rate", ctypes.c_float),
                 ("seed", ctypes.c_uint64), ("step", ctypes.c_uint32),
                 ("row_offset", ctypes.c_uint32)]
+
+
+class _PagedCacheC(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class _PagedBatchC(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_pages", ctypes.c_int), ("total_new", ctypes.c_int),
+                ("max_new", ctypes.c_int), ("page_table", ctypes.c_void_p),
+                ("cu_new", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
+
+
+class VerifyParams(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("draft_temperature", ctypes.c_float)]
 
 
 _lib = None
@@ -143,6 +162,22 @@ def load() -> ctypes.CDLL:
     lib.dd_denoise_block_adaptive.argtypes = [D, i32, P, P, P, P, P, P, P, P, P, i32, P, f32, f32,
                                               u64, u32, P, P, P, ctypes.POINTER(ctypes.c_int),
                                               P, sz, P]
+    PC, PB = ctypes.POINTER(_PagedCacheC), ctypes.POINTER(_PagedBatchC)
+    lib.dd_cache_workspace.restype = sz
+    lib.dd_cache_workspace.argtypes = []
+    lib.dd_cache_append.restype = i32
+    lib.dd_cache_append.argtypes = [PC, PB, P, i64, P, i64, P, sz, P]
+    lib.dd_cache_read.restype = i32
+    lib.dd_cache_read.argtypes = [PC, i32, i32, P, P, i32, P, P, P, sz, P]
+    lib.dd_paged_attn_workspace.restype = sz
+    lib.dd_paged_attn_workspace.argtypes = [PC, PB, i32]
+    lib.dd_paged_attn.restype = i32
+    lib.dd_paged_attn.argtypes = [PC, PB, i32, P, i64, f32, i32, P, P, P, sz, P]
+    lib.dd_verify_draft_workspace.restype = sz
+    lib.dd_verify_draft_workspace.argtypes = [i32, i32, i32]
+    lib.dd_verify_draft.restype = i32
+    lib.dd_verify_draft.argtypes = [ctypes.POINTER(VerifyParams), i32, i32, i32, i32, P, i64, P,
+                                    i64, P, P, P, P, P, P, P, P, P, sz, P]
     lib.dd_workspace_init.restype = i32
     lib.dd_workspace_init.argtypes = [P, sz, P]
     lib.dd_query_device_error.restype = i32
@@ -634,6 +669,251 @@ def denoise_block_adaptive_graph(q_steps, kc_steps, vc_steps, kp, vp, cu_prefix,
                "canvas": canvas, "canvas_history": history, "halt_step": halt,
                "steps_run": steps_run, "workspace": workspace}
     return AdaptiveGraph(h, tensors, (cu_h, temps_h))
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class _on:
+    """Makes `device` the current one around a call on its tensors."""
+    __slots__ = ("_guard",)
+
+    def __init__(self, device):
+        self._guard = (None if device.index is None or device.index == torch.cuda.current_device()
+                       else torch.cuda.device(device))
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _packed(t: torch.Tensor, heads: int, dim: int, dtype, device, what: str) -> int:
+    """Checks a packed [rows, heads, dim] tensor whose rows may lie apart (a
+    view of a fused projection) and returns the elements between rows."""
+    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim,
+          f"{what}: shape {tuple(t.shape)}, expected [rows, {heads}, {dim}]")
+    _need(t.dtype == dtype and t.device == device,
+          f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+    s = t.stride()
+    _need((dim == 1 or s[2] == 1) and (heads == 1 or s[1] == dim),
+          f"{what}: a row's [heads, dim] must be contiguous")
+    return s[0] if t.shape[0] > 1 else heads * dim
+
+
+def _dense(t: torch.Tensor, shape, dtype, device, what: str):
+    _need(tuple(t.shape) == tuple(shape),
+          f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _need(t.dtype == dtype and t.device == device,
+          f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+    _need(t.is_contiguous(), f"{what} must be contiguous")
+
+
+class PagedCache:
+    """A paged K/V cache (dd_paged_cache): k, v [num_pages, heads_kv,
+    page_size, head_dim] in bf16, or in float8_e4m3fn with uint8 k_scale,
+    v_scale [num_pages, heads_kv, page_size] (byte s stands for 2^(s - 127)).
+    The tensors stay the caller's; the object keeps them alive."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        _need(k.is_cuda and k.numel() > 0, "k: a non-empty CUDA tensor is needed")
+        _need(k.dim() == 4, f"k: shape {tuple(k.shape)}, expected [pages, heads, page_size, dim]")
+        _dense(k, k.shape, k.dtype, k.device, "k")
+        _dense(v, k.shape, k.dtype, k.device, "v")
+        self.device, code = k.device, _dtype_code(k)
+        if code == DD_E4M3:
+            _need(k_scale is not None and v_scale is not None,
+                  "an E4M3 cache needs k_scale and v_scale")
+            for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _dense(t, k.shape[:3], torch.uint8, k.device, what)
+        else:
+            _need(k_scale is None and v_scale is None, "only an E4M3 cache has scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads_kv, self.page_size, self.head_dim = k.shape
+
+        def at(t):
+            return None if t is None else t.data_ptr()
+
+        self._c = _PagedCacheC(self.num_pages, self.page_size, self.heads_kv, self.head_dim, code,
+                               at(k), at(v), at(k_scale), at(v_scale))
+        self._ref = ctypes.byref(self._c)
+
+
+def new_paged_cache(num_pages: int, page_size: int, heads_kv: int, head_dim: int,
+                    dtype=torch.bfloat16, device="cuda") -> PagedCache:
+    """An empty PagedCache of bf16 or float8_e4m3fn."""
+    shape = (num_pages, heads_kv, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return PagedCache(k, v)
+    return PagedCache(k, v, *(torch.full(shape[:3], 127, dtype=torch.uint8, device=device)
+                              for _ in range(2)))
+
+
+class PagedBatch:
+    """The sequences of a call over a PagedCache (dd_paged_batch): page_table
+    int32 [B, max_pages], cu_new int32 [B+1], kv_len int32 [B] (with the new
+    tokens), all on the device; max_new bounds any sequence's new tokens.
+    Their contents may change between calls; the tensors are kept alive."""
+
+    def __init__(self, page_table: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor,
+                 max_new: int):
+        _need(page_table.dim() == 2, "page_table must be [batch, max_pages]")
+        B, pages = page_table.shape
+        self.device = page_table.device
+        _need(page_table.is_cuda, "page_table must be a CUDA tensor")
+        _dense(page_table, (B, pages), torch.int32, self.device, "page_table")
+        _dense(cu_new, (B + 1,), torch.int32, self.device, "cu_new")
+        _dense(kv_len, (B,), torch.int32, self.device, "kv_len")
+        self.page_table, self.cu_new, self.kv_len, self.max_new = page_table, cu_new, kv_len, max_new
+        self.batch = B
+        self._args = (B, pages)
+        self._ptrs = (page_table.data_ptr(), cu_new.data_ptr(), kv_len.data_ptr())
+
+    def _c(self, total_new: int):
+        return _PagedBatchC(*self._args, total_new, int(self.max_new), *self._ptrs)
+
+
+def cache_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor,
+                 workspace=None, stream=None):
+    """dd_cache_append: writes bf16 k_new, v_new [total_new, heads_kv,
+    head_dim] (rows may lie apart) at the batch's last positions."""
+    lib, dev = load(), cache.device
+    _need(batch.device == dev, f"batch on {batch.device}, cache on {dev}")
+    ks = _packed(k_new, cache.heads_kv, cache.head_dim, torch.bfloat16, dev, "k_new")
+    vs = _packed(v_new, cache.heads_kv, cache.head_dim, torch.bfloat16, dev, "v_new")
+    _need(k_new.shape[0] == v_new.shape[0], "k_new and v_new have different numbers of rows")
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(int(lib.dd_cache_workspace()), dev, stream)
+        _check(lib.dd_cache_append(cache._ref, batch._c(k_new.shape[0]), k_new.data_ptr(), ks,
+                                   v_new.data_ptr(), vs, workspace.data_ptr(), workspace.numel(),
+                                   _stream(stream)))
+
+
+def cache_read(cache: PagedCache, page_table: torch.Tensor, cu_prefix: torch.Tensor,
+               total: Optional[int] = None, k_out=None, v_out=None, workspace=None, stream=None):
+    """dd_cache_read: the first cu_prefix[b+1] - cu_prefix[b] positions of
+    every sequence, packed as canvas_attn takes them.  Returns (kp, vp), bf16
+    [total, heads_kv, head_dim]; total defaults to k_out's rows."""
+    lib, dev = load(), cache.device
+    _need(page_table.dim() == 2, "page_table must be [batch, max_pages]")
+    B, pages = page_table.shape
+    _dense(page_table, (B, pages), torch.int32, dev, "page_table")
+    _dense(cu_prefix, (B + 1,), torch.int32, dev, "cu_prefix")
+    _need(total is not None or k_out is not None, "cache_read needs total or k_out")
+    total = k_out.shape[0] if total is None else int(total)
+    _need(total >= 0, f"total={total}")
+    shape = (total, cache.heads_kv, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _dense(k_out, shape, torch.bfloat16, dev, "k_out")
+    _dense(v_out, shape, torch.bfloat16, dev, "v_out")
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(int(lib.dd_cache_workspace()), dev, stream)
+        _check(lib.dd_cache_read(cache._ref, B, pages, page_table.data_ptr(),
+                                 cu_prefix.data_ptr(), total, k_out.data_ptr(), v_out.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return k_out, v_out
+
+
+def paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, total_new: int,
+                               heads_q: int) -> int:
+    return int(load().dd_paged_attn_workspace(cache._ref, batch._c(total_new), heads_q))
+
+
+def paged_attn(q: torch.Tensor, cache: PagedCache, batch: PagedBatch,
+               scale: Optional[float] = None, causal: bool = True, out=None, lse=None,
+               want_lse: bool = False, workspace=None, stream=None):
+    """dd_paged_attn: attention of the batch's new tokens, q bf16 [total_new,
+    heads_q, head_dim] (rows may lie apart), over the cache that holds their
+    own K and V.  Returns (out [total_new, heads_q, head_dim], lse
+    [total_new, heads_q] or None)."""
+    lib, dev, D = load(), cache.device, cache.head_dim
+    _need(q.dim() == 3, "q must be [total_new, heads_q, head_dim]")
+    T, Hq = q.shape[0], q.shape[1]
+    qs = _packed(q, Hq, D, torch.bfloat16, dev, "q")
+    _need(batch.device == dev, f"batch on {batch.device}, cache on {dev}")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    _dense(out, (T, Hq, D), torch.bfloat16, dev, "out")
+    if want_lse and lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _dense(lse, (T, Hq), torch.float32, dev, "lse")
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(paged_attn_workspace_bytes(cache, batch, T, Hq), dev, stream)
+        _check(lib.dd_paged_attn(cache._ref, batch._c(T), Hq, q.data_ptr(), qs,
+                                 float(scale if scale is not None else D ** -0.5), int(causal),
+                                 out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return out, lse
+
+
+def verify_draft_workspace_bytes(batch: int, total: int, vocab: int) -> int:
+    return int(load().dd_verify_draft_workspace(batch, total, vocab))
+
+
+def verify_draft_outputs(batch: int, total: int, device="cuda") -> dict:
+    """The output tensors of verify_draft: accepted, tokens, target_prob."""
+    return {"accepted": torch.empty(batch, dtype=torch.int32, device=device),
+            "tokens": torch.empty(total + batch, dtype=torch.int32, device=device),
+            "target_prob": torch.empty(total, dtype=torch.float32, device=device)}
+
+
+def verify_draft(target_logits: torch.Tensor, draft_logits: torch.Tensor,
+                 draft_tokens: torch.Tensor, draft_conf: torch.Tensor, cu_draft: torch.Tensor,
+                 u_accept: torch.Tensor, u_sample: torch.Tensor, temperature: float = 1.0,
+                 draft_temperature: float = 1.0, outputs: Optional[dict] = None, workspace=None,
+                 stream=None) -> dict:
+    """dd_verify_draft: checks drafted tokens (pred and conf of
+    sample_renoise over draft_logits [T, V]) against target_logits [T + B, V]
+    (sequence b's rows start at cu_draft[b] + b; one more than its drafts).
+    Returns the dict of verify_draft_outputs: accepted [B], tokens [T + B]
+    (accepted tokens, the next token, -1), target_prob [T]."""
+    lib, dev = load(), target_logits.device
+    _need(target_logits.is_cuda, "target_logits must be a CUDA tensor")
+    _need(target_logits.dim() == 2 and draft_logits.dim() == 2, "logits must be 2-D")
+    T, V = draft_logits.shape
+    B = u_sample.numel()
+    _need(tuple(target_logits.shape) == (T + B, V),
+          f"target_logits: shape {tuple(target_logits.shape)}, expected {(T + B, V)}")
+    for t, what in ((target_logits, "target_logits"), (draft_logits, "draft_logits")):
+        _need(t.dtype == target_logits.dtype and t.device == dev,
+              f"{what}: {t.dtype} on {t.device}, expected {target_logits.dtype} on {dev}")
+        _need(V == 1 or t.stride(1) == 1, f"{what}: a row must be contiguous")
+    for t, n, dt, what in ((draft_tokens, T, torch.int32, "draft_tokens"),
+                           (draft_conf, T, torch.float32, "draft_conf"),
+                           (cu_draft, B + 1, torch.int32, "cu_draft"),
+                           (u_accept, T, torch.float32, "u_accept"),
+                           (u_sample, B, torch.float32, "u_sample")):
+        _dense(t, (n,), dt, dev, what)
+    o = outputs if outputs is not None else verify_draft_outputs(B, T, dev)
+    for name, n, dt in (("accepted", B, torch.int32), ("tokens", T + B, torch.int32),
+                        ("target_prob", T, torch.float32)):
+        _dense(o[name], (n,), dt, dev, name)
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(verify_draft_workspace_bytes(B, T, V), dev, stream)
+        prm = VerifyParams(float(temperature), float(draft_temperature))
+        _check(lib.dd_verify_draft(
+            ctypes.byref(prm), _dtype_code(target_logits), B, T, V, target_logits.data_ptr(),
+            target_logits.stride(0) if T + B > 1 else V, draft_logits.data_ptr(),
+            draft_logits.stride(0) if T > 1 else V, draft_tokens.data_ptr(),
+            draft_conf.data_ptr(), cu_draft.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
+            o["accepted"].data_ptr(), o["tokens"].data_ptr(), o["target_prob"].data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return o
 
 
 def query_device_error(workspace: torch.Tensor, stream=None):

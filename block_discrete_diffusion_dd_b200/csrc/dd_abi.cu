@@ -1085,6 +1085,274 @@ dd_status dd_denoise_block_adaptive_graph_destroy(dd_adaptive_graph g) {
   return DD_OK;
 }
 
+// ------------------------------------------------- paged cache and drafts
+namespace {
+
+dd_status check_cache(const dd_paged_cache* c, bool pointers) {
+  if (!c) return fail(DD_ERR_INVALID_ARG, "cache is NULL");
+  if (c->dtype != DD_BF16 && c->dtype != DD_F32 && c->dtype != DD_E4M3)
+    return fail(DD_ERR_INVALID_ARG, "unknown cache dtype %d", (int)c->dtype);
+  if (c->dtype == DD_F32) return fail(DD_ERR_UNSUPPORTED, "a cache is DD_BF16 or DD_E4M3");
+  if (c->num_pages < 1 || c->heads_kv < 1)
+    return fail(DD_ERR_INVALID_ARG, "num_pages=%d heads_kv=%d", c->num_pages, c->heads_kv);
+  if (c->page_size < 1) return fail(DD_ERR_INVALID_ARG, "page_size=%d", c->page_size);
+  if (c->page_size < 8 || c->page_size > 512 || (c->page_size & (c->page_size - 1)))
+    return fail(DD_ERR_UNSUPPORTED, "page_size %d (a power of two, 8..512)", c->page_size);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(DD_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", c->head_dim);
+  if ((int64_t)c->num_pages * c->heads_kv > INT32_MAX)
+    return fail(DD_ERR_UNSUPPORTED, "num_pages * heads_kv exceeds 2^31");
+  if (!pointers) return DD_OK;
+  if (!c->k || !c->v) return fail(DD_ERR_INVALID_ARG, "NULL cache pointer");
+  if (!aligned16(c->k) || !aligned16(c->v))
+    return fail(DD_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  if (c->dtype == DD_E4M3) {
+    if (!c->k_scale || !c->v_scale) return fail(DD_ERR_INVALID_ARG, "NULL cache scale pointer");
+    if (!aligned16(c->k_scale) || !aligned16(c->v_scale))
+      return fail(DD_ERR_INVALID_ARG, "cache scale pointers must be 16-byte aligned");
+  }
+  return DD_OK;
+}
+
+dd_status check_paged_batch(const dd_paged_cache* c, const dd_paged_batch* b, bool pointers) {
+  if (!b) return fail(DD_ERR_INVALID_ARG, "batch is NULL");
+  if (b->batch < 0 || b->total_new < 0 || b->max_new < 0 || b->max_pages < 1)
+    return fail(DD_ERR_INVALID_ARG, "batch=%d total_new=%d max_new=%d max_pages=%d", b->batch,
+                b->total_new, b->max_new, b->max_pages);
+  if ((int64_t)b->max_pages * c->page_size > INT32_MAX)
+    return fail(DD_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^31");
+  if (!pointers || b->batch == 0) return DD_OK;
+  if (!b->page_table || !b->cu_new || !b->kv_len)
+    return fail(DD_ERR_INVALID_ARG, "NULL page_table, cu_new or kv_len");
+  return DD_OK;
+}
+
+dd_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(DD_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (have < need)
+    return fail(DD_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", have, need);
+  return DD_OK;
+}
+
+PagedBatch paged_batch(const dd_paged_cache* c, const dd_paged_batch* b) {
+  PagedBatch p{};
+  p.batch = b->batch;
+  p.max_pages = b->max_pages;
+  p.total_new = b->total_new;
+  p.max_new = b->max_new;
+  p.heads_kv = c->heads_kv;
+  p.head_dim = c->head_dim;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+  p.num_pages = c->num_pages;
+  p.page_table = b->page_table;
+  p.cu_new = b->cu_new;
+  p.kv_len = b->kv_len;
+  return p;
+}
+
+PagedPool paged_pool(const dd_paged_cache* c) {
+  return PagedPool{c->dtype == DD_E4M3, c->k, c->v, c->k_scale, c->v_scale};
+}
+
+// Rows of one call that a grid of (token, head, K or V) units covers.
+dd_status check_cache_units(int64_t rows, int heads_kv) {
+  if (rows * 2 * heads_kv > INT32_MAX)
+    return fail(DD_ERR_UNSUPPORTED, "tokens * 2 * heads_kv exceeds 2^31");
+  return DD_OK;
+}
+
+dd_status check_stride(const char* what, int64_t stride, int64_t least) {
+  if (stride < least || stride % 8 != 0)
+    return fail(DD_ERR_INVALID_ARG, "%s (%lld) must be >= %lld and a multiple of 8", what,
+                (long long)stride, (long long)least);
+  return DD_OK;
+}
+
+dd_status check_heads_q(int heads_q, int heads_kv) {
+  if (heads_q < 1 || heads_q % heads_kv != 0)
+    return fail(DD_ERR_INVALID_ARG, "heads_q (%d) is not a multiple of heads_kv (%d)", heads_q,
+                heads_kv);
+  if (heads_q / heads_kv > 128)
+    return fail(DD_ERR_UNSUPPORTED, "heads_q / heads_kv = %d (up to 128)", heads_q / heads_kv);
+  return DD_OK;
+}
+
+}  // namespace
+
+size_t dd_cache_workspace(void) { return kHeaderBytes; }
+
+dd_status dd_cache_append(const dd_paged_cache* cache, const dd_paged_batch* batch,
+                          const void* k_new, int64_t k_stride, const void* v_new,
+                          int64_t v_stride, void* workspace, size_t workspace_bytes,
+                          dd_stream_t stream) {
+  g_last_error.clear();
+  dd_status st = check_cache(cache, true);
+  if (st != DD_OK) return st;
+  if ((st = check_paged_batch(cache, batch, true)) != DD_OK) return st;
+  const int64_t row = (int64_t)cache->heads_kv * cache->head_dim;
+  if ((st = check_stride("k_stride", k_stride, row)) != DD_OK) return st;
+  if ((st = check_stride("v_stride", v_stride, row)) != DD_OK) return st;
+  if ((st = check_cache_units(batch->total_new, cache->heads_kv)) != DD_OK) return st;
+  if (batch->batch == 0 || batch->total_new == 0) return DD_OK;
+  if (!k_new || !v_new) return fail(DD_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(k_new) || !aligned16(v_new))
+    return fail(DD_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, kHeaderBytes)) != DD_OK) return st;
+  CacheAppendArgs a{};
+  a.p = paged_batch(cache, batch);
+  a.pool = paged_pool(cache);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.err = static_cast<uint32_t*>(workspace);
+  cudaError_t e = launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache append");
+  return DD_OK;
+}
+
+dd_status dd_cache_read(const dd_paged_cache* cache, int batch, int max_pages,
+                        const int32_t* page_table, const int32_t* cu_prefix, int total,
+                        void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                        dd_stream_t stream) {
+  g_last_error.clear();
+  dd_status st = check_cache(cache, true);
+  if (st != DD_OK) return st;
+  // (the lengths array that a batch has besides is not used here)
+  const dd_paged_batch pb = {batch, max_pages, total, 0, page_table, cu_prefix, cu_prefix};
+  if ((st = check_paged_batch(cache, &pb, true)) != DD_OK) return st;
+  if ((st = check_cache_units(total, cache->heads_kv)) != DD_OK) return st;
+  if (batch == 0 || total == 0) return DD_OK;
+  if (!k_out || !v_out) return fail(DD_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(k_out) || !aligned16(v_out))
+    return fail(DD_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, kHeaderBytes)) != DD_OK) return st;
+  CacheReadArgs a{};
+  a.p = paged_batch(cache, &pb);
+  a.pool = paged_pool(cache);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.err = static_cast<uint32_t*>(workspace);
+  cudaError_t e = launch_cache_read(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read");
+  return DD_OK;
+}
+
+size_t dd_paged_attn_workspace(const dd_paged_cache* cache, const dd_paged_batch* batch,
+                               int heads_q) {
+  if (check_cache(cache, false) != DD_OK || check_paged_batch(cache, batch, false) != DD_OK ||
+      check_heads_q(heads_q, cache->heads_kv) != DD_OK)
+    return 0;
+  PagedAttnArgs a{};
+  a.p = paged_batch(cache, batch);
+  a.pool = paged_pool(cache);
+  a.heads_q = heads_q;
+  return kHeaderBytes + paged_attn_scratch_bytes(a);
+}
+
+dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch, int heads_q,
+                        const void* q, int64_t q_stride, float scale, int causal, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, dd_stream_t stream) {
+  g_last_error.clear();
+  dd_status st = check_cache(cache, true);
+  if (st != DD_OK) return st;
+  if ((st = check_paged_batch(cache, batch, true)) != DD_OK) return st;
+  if ((st = check_heads_q(heads_q, cache->heads_kv)) != DD_OK) return st;
+  if ((st = check_stride("q_stride", q_stride, (int64_t)heads_q * cache->head_dim)) != DD_OK)
+    return st;
+  if (!std::isfinite(scale) || scale <= 0.f)
+    return fail(DD_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if ((int64_t)batch->total_new * heads_q > INT32_MAX)
+    return fail(DD_ERR_UNSUPPORTED, "total_new * heads_q exceeds 2^31");
+  if (batch->batch == 0 || batch->total_new == 0) return DD_OK;
+  if (!q || !out) return fail(DD_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(out))
+    return fail(DD_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  PagedAttnArgs a{};
+  a.p = paged_batch(cache, batch);
+  a.pool = paged_pool(cache);
+  a.heads_q = heads_q;
+  if ((st = check_workspace(workspace, workspace_bytes,
+                            kHeaderBytes + paged_attn_scratch_bytes(a))) != DD_OK)
+    return st;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.out = out;
+  a.lse = lse;
+  a.err = static_cast<uint32_t*>(workspace);
+  a.scratch = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+  cudaError_t e = launch_paged_attn(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention");
+  return DD_OK;
+}
+
+size_t dd_verify_draft_workspace(int batch, int total, int vocab) {
+  if (batch < 0 || total < 0 || vocab < 1) return 0;
+  return kHeaderBytes + verify_scratch_bytes(batch, total, vocab);
+}
+
+dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int batch, int total,
+                          int vocab, const void* target_logits, int64_t target_stride,
+                          const void* draft_logits, int64_t draft_stride,
+                          const int32_t* draft_tokens, const float* draft_conf,
+                          const int32_t* cu_draft, const float* u_accept, const float* u_sample,
+                          int32_t* accepted, int32_t* tokens, float* target_prob,
+                          void* workspace, size_t workspace_bytes, dd_stream_t stream) {
+  g_last_error.clear();
+  if (!params) return fail(DD_ERR_INVALID_ARG, "params is NULL");
+  if (dtype != DD_BF16 && dtype != DD_F32)
+    return fail(DD_ERR_INVALID_ARG, "unknown dtype %d (logits are bf16 or fp32)", (int)dtype);
+  if (batch < 0 || total < 0 || vocab < 1)
+    return fail(DD_ERR_INVALID_ARG, "batch=%d total=%d vocab=%d", batch, total, vocab);
+  if (target_stride < vocab || draft_stride < vocab)
+    return fail(DD_ERR_INVALID_ARG, "row strides (%lld, %lld) < vocab (%d)",
+                (long long)target_stride, (long long)draft_stride, vocab);
+  const float taus[2] = {params->temperature, params->draft_temperature};
+  for (float t : taus)
+    if (!std::isfinite(t) || t < 1e-3f)
+      return fail(DD_ERR_INVALID_ARG, "temperatures must be finite and >= 1e-3");
+  if (((int64_t)total + batch) * (((int64_t)vocab + 2047) / 2048) > INT32_MAX)
+    return fail(DD_ERR_UNSUPPORTED, "rows * chunks exceeds 2^31");
+  if (batch == 0) return DD_OK;
+  if (!target_logits || !cu_draft || !u_sample || !accepted || !tokens)
+    return fail(DD_ERR_INVALID_ARG, "NULL required pointer");
+  if (total > 0 && (!draft_logits || !draft_tokens || !draft_conf || !u_accept || !target_prob))
+    return fail(DD_ERR_INVALID_ARG, "NULL required pointer");
+  if (!aligned16(target_logits) || (total > 0 && !aligned16(draft_logits)))
+    return fail(DD_ERR_INVALID_ARG, "logits pointers must be 16-byte aligned");
+  dd_status st = check_workspace(workspace, workspace_bytes,
+                                 kHeaderBytes + verify_scratch_bytes(batch, total, vocab));
+  if (st != DD_OK) return st;
+  VerifyArgs a{};
+  a.target = target_logits;
+  a.draft = total > 0 ? draft_logits : target_logits;  // no drafts: never read
+  a.bf16 = dtype == DD_BF16;
+  a.batch = batch;
+  a.total = total;
+  a.vocab = vocab;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.tau = params->temperature;
+  a.draft_tau = params->draft_temperature;
+  a.draft_tokens = draft_tokens;
+  a.draft_conf = draft_conf;
+  a.cu_draft = cu_draft;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.accepted = accepted;
+  a.tokens = tokens;
+  a.target_prob = target_prob;
+  a.err = static_cast<uint32_t*>(workspace);
+  a.scratch = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+  cudaError_t e = launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "draft verification");
+  return DD_OK;
+}
+
 dd_status dd_workspace_init(void* workspace, size_t workspace_bytes, dd_stream_t stream) {
   g_last_error.clear();
   if (!workspace || workspace_bytes < kHeaderBytes)

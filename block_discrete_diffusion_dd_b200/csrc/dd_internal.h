@@ -163,6 +163,76 @@ DensePlan dense_plan(int rows, int K, int N);
 size_t dense_partial_bytes(int rows, int K, int N);
 cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream);
 
+// A batch of sequences over a paged cache (device arrays), with the parts of
+// the cache's geometry that address it.  For cache_read, cu_new / total_new
+// are the packed prefix's offsets and rows, and kv_len and max_new are unused.
+struct PagedBatch {
+  int batch, max_pages, total_new, max_new;
+  int heads_kv, head_dim, page_shift, num_pages;
+  const int32_t* page_table;  // [batch, max_pages]
+  const int32_t* cu_new;      // [batch + 1]
+  const int32_t* kv_len;      // [batch]
+};
+struct PagedPool {
+  bool e4m3;
+  void *k, *v;                  // [num_pages, heads_kv, page_size, head_dim]
+  uint8_t *k_scale, *v_scale;   // E4M3: [num_pages, heads_kv, page_size]
+};
+
+// The paged cache (dd_cache.cu); pointers 16-byte aligned, strides multiples
+// of 8 elements, rows * heads within the grid, validated by the ABI layer.
+struct CacheAppendArgs {
+  PagedBatch p;
+  PagedPool pool;
+  const void *k_new, *v_new;  // bf16 [total_new, heads_kv, head_dim]
+  int64_t k_stride, v_stride;
+  uint32_t* err;
+};
+cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t stream);
+struct CacheReadArgs {
+  PagedBatch p;
+  PagedPool pool;
+  void *k_out, *v_out;  // bf16 [total_new, heads_kv, head_dim]
+  uint32_t* err;
+};
+cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t stream);
+
+// Attention of a chunk of new tokens over the paged cache (dd_paged_attn.cu).
+struct PagedAttnArgs {
+  PagedBatch p;
+  PagedPool pool;
+  int heads_q;
+  const void* q;  // bf16 [total_new, heads_q, head_dim]
+  int64_t q_stride;
+  float scale;
+  bool causal;
+  void* out;   // bf16 [total_new, heads_q, head_dim]
+  float* lse;  // fp32 [total_new, heads_q] or NULL
+  uint32_t* err;
+  void* scratch;  // paged_attn_scratch_bytes
+};
+size_t paged_attn_scratch_bytes(const PagedAttnArgs& a);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
+// Verification of drafted tokens (dd_verify.cu).
+struct VerifyArgs {
+  const void *target, *draft;
+  bool bf16;
+  int batch, total, vocab;  // total: drafted tokens; target has total + batch rows
+  int64_t target_stride, draft_stride;
+  double tau, draft_tau;
+  const int32_t* draft_tokens;
+  const float* draft_conf;
+  const int32_t* cu_draft;
+  const float *u_accept, *u_sample;
+  int32_t *accepted, *tokens;
+  float* target_prob;
+  uint32_t* err;
+  void* scratch;  // verify_scratch_bytes
+};
+size_t verify_scratch_bytes(int batch, int total, int vocab);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+
 // Time limit of the pipeline waits (mbarrier waits that can abort) of the
 // tensor-core kernels launched from this host thread: 1 s unless a test
 // stall is set (dd_set_test_stall_ns).  Waits that drain in-flight copies

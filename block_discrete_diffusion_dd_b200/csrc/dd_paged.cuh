@@ -1,0 +1,69 @@
+// dd_paged.cuh -- device-side view of a paged batch (dd_paged_batch), shared
+// by the cache kernels and the attention over the cache.
+//
+// Lengths, offsets and page ids live in device memory, where the host cannot
+// check them before a launch, so every kernel checks what it uses: a batch
+// row with impossible lengths is taken as empty, a page id outside the pool
+// is never followed, and both latch kDevErrBounds in the workspace header.
+#pragma once
+
+#include "dd_device.cuh"
+#include "dd_internal.h"
+
+namespace dd {
+
+struct ChunkRow {
+  int q0;   // first row of the packed new-token tensors
+  int n;    // new tokens
+  int len;  // tokens in the cache, the new ones included
+};
+
+__device__ __forceinline__ ChunkRow chunk_row(const PagedBatch& p, int b, uint32_t* err) {
+  ChunkRow r;
+  r.q0 = __ldg(p.cu_new + b);
+  const int q1 = __ldg(p.cu_new + b + 1);
+  r.len = __ldg(p.kv_len + b);
+  r.n = q1 - r.q0;
+  if (r.q0 < 0 || q1 < r.q0 || q1 > p.total_new || r.n > p.max_new || r.len < 0 ||
+      (int64_t)r.len > ((int64_t)p.max_pages << p.page_shift)) {
+    atomicOr(err, kDevErrBounds);
+    r.q0 = r.n = r.len = 0;
+  }
+  return r;
+}
+
+// The batch row that owns packed row t: the last b with cu[b] <= t (rows of
+// no tokens are passed over), or -1 when t lies at or past cu[batch].
+__device__ __forceinline__ int owner_row(const int32_t* cu, int batch, int t) {
+  if (t >= __ldg(cu + batch) || t < __ldg(cu)) return -1;
+  int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The pool row of position `pos` of batch row b for kv head 0, in units of
+// one head's token: the row of head h is h << page_shift further on.  -1
+// (and the error latched) for a page id outside the pool.
+__device__ __forceinline__ int64_t pool_row(const PagedBatch& p, int b, int pos, uint32_t* err) {
+  const int page = __ldg(p.page_table + (int64_t)b * p.max_pages + (pos >> p.page_shift));
+  if ((uint32_t)page >= (uint32_t)p.num_pages) {
+    atomicOr(err, kDevErrBounds);
+    return -1;
+  }
+  return (((int64_t)page * p.heads_kv) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+}
+
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((127 + e) << 23); }
+
+// Two E4M3 bytes (low byte first) as floats; exact, NaN stays NaN.
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+}  // namespace dd

@@ -492,6 +492,173 @@ DD_API dd_status dd_denoise_block_adaptive_graph_launch(dd_adaptive_graph graph,
                                                         dd_stream_t stream);
 DD_API dd_status dd_denoise_block_adaptive_graph_destroy(dd_adaptive_graph graph);
 
+/* ---- The paged cache and the path that commits a block.  The canvas is
+ * denoised against "the causally encoded cache" ("DiffusionGemma Technical
+ * Report", "The mechanism"); the calls below grow that cache and read it: the
+ * K and V of new tokens (a finished block, a chunk of a prompt, one token)
+ * are appended to it, the new tokens are encoded by causal attention over
+ * it, drafted tokens are checked against an autoregressive target, and the
+ * cache is laid out as the packed prefix that dd_canvas_attn takes.
+ *
+ * The lengths are device arrays, so a captured call serves every later
+ * length up to its bounds, and the host is never waited for.  What they hold
+ * is checked on the device: a batch row with impossible values (see
+ * dd_paged_batch) is taken as empty, a page id outside the pool is never
+ * followed, and both latch DD_ERR_DEVICE_BOUNDS in the workspace.  Their
+ * workspaces need no state between calls beyond the error word, so calls of
+ * any shape may share one, as long as they do not overlap in time. */
+
+/* A cache of pages.  One page holds page_size consecutive positions of one
+ * sequence, for every kv head.
+ *   num_pages   >= 1
+ *   page_size   a power of two, 8..512
+ *   heads_kv    >= 1;  head_dim 64 or 128
+ *   dtype       DD_BF16 or DD_E4M3
+ *   k, v        [num_pages, heads_kv, page_size, head_dim] of dtype
+ *   k_scale, v_scale  uint8 [num_pages, heads_kv, page_size] for DD_E4M3:
+ *               byte s scales its (position, head) by 2^(s - 127) (the E8M0
+ *               encoding; the library writes 7..247, and reading takes
+ *               1..254); ignored for DD_BF16 */
+typedef struct {
+  int num_pages, page_size, heads_kv, head_dim;
+  dd_dtype dtype;
+  void *k, *v;
+  uint8_t *k_scale, *v_scale;
+} dd_paged_cache;
+
+/* A batch of sequences with new tokens, packed one after the other.
+ *   batch       B >= 0 sequences
+ *   max_pages   entries per row of page_table; max_pages * page_size < 2^31
+ *   total_new   rows of the packed new-token tensors; rows at or past
+ *               cu_new[B] belong to no sequence, are not read, and their
+ *               outputs are left as they were
+ *   max_new     no sequence has more new tokens than this
+ *   page_table  int32 [B, max_pages]: position p of sequence b lies in page
+ *               page_table[b, p / page_size]; entries past the sequence's
+ *               length are not read
+ *   cu_new      int32 [B + 1]: sequence b has the packed rows cu_new[b] ..
+ *               cu_new[b+1] - 1 (none if equal)
+ *   kv_len      int32 [B]: its length with the new tokens, which are its
+ *               last ones: packed row cu_new[b] + i is position
+ *               kv_len[b] - n + i, n = cu_new[b+1] - cu_new[b]
+ * A row is impossible, and taken as empty, unless 0 <= cu_new[b] <=
+ * cu_new[b+1] <= total_new, n <= max_new and 0 <= kv_len[b] <=
+ * max_pages * page_size.  kv_len[b] < n is possible: positions below 0 are
+ * not stored and see nothing. */
+typedef struct {
+  int batch, max_pages, total_new, max_new;
+  const int32_t *page_table, *cu_new, *kv_len;
+} dd_paged_batch;
+
+/* Workspace bytes of dd_cache_append and dd_cache_read (the error word). */
+DD_API size_t dd_cache_workspace(void);
+
+/* Writes the K and V of the new tokens into the cache.
+ *   k_new, v_new  bf16 [total_new, heads_kv, head_dim] with k_stride /
+ *                 v_stride elements between tokens (>= heads_kv * head_dim,
+ *                 a multiple of 8): views of a fused projection are taken
+ *   workspace     >= dd_cache_workspace() bytes, 256-byte aligned
+ * A DD_BF16 cache takes the bits as they are.  A DD_E4M3 cache takes, per
+ * (token, head), with a the largest finite magnitude of its head_dim values,
+ * the scale 2^e of the least integer e with a <= 448 * 2^e (within
+ * [-120, 120]; 0 when a = 0) and the codes E4M3(x * 2^-e), rounded to
+ * nearest even (at e = 120 to 240 at most: 256 * 2^120 is no bf16 number);
+ * infinities and NaN become NaN.  Two tokens of one call that
+ * share a slot (page_table rows that share a page) leave one of them or a
+ * mixture. */
+DD_API dd_status dd_cache_append(const dd_paged_cache* cache, const dd_paged_batch* batch,
+                                 const void* k_new, int64_t k_stride, const void* v_new,
+                                 int64_t v_stride, void* workspace, size_t workspace_bytes,
+                                 dd_stream_t stream);
+
+/* Reads the first cu_prefix[b+1] - cu_prefix[b] positions of every sequence
+ * back, packed: the k_prefix, v_prefix and cu_prefix of dd_canvas_attn.  The
+ * values are exact (an E4M3 code times a power of two is a bf16 number).
+ *   page_table    int32 [batch, max_pages]
+ *   cu_prefix     device int32 [batch + 1], 0 <= cu_prefix[0], non-decreasing
+ *   total         rows of the outputs; rows outside [cu_prefix[0],
+ *                 cu_prefix[batch]) are left as they were, and so are rows
+ *                 whose position or page does not exist (which latch
+ *                 DD_ERR_DEVICE_BOUNDS)
+ *   k_out, v_out  bf16 [total, heads_kv, head_dim] */
+DD_API dd_status dd_cache_read(const dd_paged_cache* cache, int batch, int max_pages,
+                               const int32_t* page_table, const int32_t* cu_prefix, int total,
+                               void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                               dd_stream_t stream);
+
+/* Workspace bytes of dd_paged_attn (0 on invalid arguments).  The pointers
+ * of `cache` and `batch` are not read. */
+DD_API size_t dd_paged_attn_workspace(const dd_paged_cache* cache, const dd_paged_batch* batch,
+                                      int heads_q);
+
+/* Attention of the new tokens over the paged cache, which holds their own K
+ * and V already (dd_cache_append).  Query head h reads kv head
+ * h / (heads_q / heads_kv).  Token i of sequence b sees its positions
+ *   j < kv_len[b] - n + i + 1   (causal != 0: the encoding of a block, a
+ *                               prompt or a decoded token)
+ *   j < kv_len[b]               (causal == 0: a canvas, as dd_canvas_attn)
+ * under one softmax: out = sum_j softmax_j(scale * <q, k_j>) v_j.  A token
+ * that sees nothing gets out = 0 and lse = -inf.
+ *   heads_q    a multiple of heads_kv, any ratio up to 128
+ *   q          bf16 [total_new, heads_q, head_dim] with q_stride elements
+ *              between tokens (>= heads_q * head_dim, a multiple of 8)
+ *   scale      finite, > 0
+ *   out        bf16 [total_new, heads_q, head_dim]
+ *   lse        optional fp32 [total_new, heads_q]
+ *   workspace  >= dd_paged_attn_workspace(...) bytes, 256-byte aligned
+ * What the cache holds at positions >= kv_len[b] does not matter (NaN
+ * included); below kv_len[b] it has to be finite, also where a causal mask
+ * hides it from some of the tokens. */
+DD_API dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch,
+                               int heads_q, const void* q, int64_t q_stride, float scale,
+                               int causal, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, dd_stream_t stream);
+
+/* Verification of drafted tokens against a target's probabilities, from
+ * given random numbers.  Sequence b drafted k_b = cu_draft[b+1] -
+ * cu_draft[b] tokens x_i, each drawn with probability conf_i from
+ * q_i = softmax(draft_logits_i / draft_temperature) -- for a denoised block,
+ * `pred` and `conf` of dd_sample_renoise; the target gives p_i =
+ * softmax(target_logits_i / temperature) for i = 0 .. k_b.  With u_i in
+ * [0, 1):
+ *   n_b    = the first i with u_i * conf_i >= p_i(x_i), or k_b
+ *   weights  w = max(p_n - q_n, 0) where n_b < k_b (p_n if that is 0
+ *            everywhere), w = p_k where n_b = k_b
+ *   next   = the least v with w_0 + .. + w_v > u_sample_b * sum(w); the last
+ *            v with w_v > 0 should rounding leave none; -1 if sum(w) = 0
+ * Tokens that follow are distributed as the target's samples.  The
+ * probabilities that decide are formed in 64 bits.
+ *   params         temperature, draft_temperature: finite, >= 1e-3
+ *   dtype          of both logits: DD_BF16 or DD_F32; finite or -inf
+ *   batch, total   B sequences, rows of the packed draft tensors
+ *   target_logits  [total + B, vocab], target_stride elements between rows:
+ *                  sequence b's k_b + 1 rows start at cu_draft[b] + b
+ *   draft_logits   [total, vocab], draft_stride elements between rows
+ *   draft_tokens   int32 [total];  draft_conf fp32 [total]
+ *   cu_draft       device int32 [B + 1]; a row outside [0, total] or
+ *                  decreasing, like a token outside the vocabulary, latches
+ *                  DD_ERR_DEVICE_BOUNDS (the row gets accepted = 0 and no
+ *                  tokens; the token is refused)
+ *   u_accept       fp32 [total];  u_sample fp32 [B]
+ *   accepted       int32 [B]: n_b
+ *   tokens         int32 [total + B]: from cu_draft[b] + b on, the n_b
+ *                  accepted tokens, the next token, and -1
+ *   target_prob    fp32 [total]: p_i(x_i)
+ *   workspace      >= dd_verify_draft_workspace(...) bytes, 256-byte
+ *                  aligned (0 from the query on invalid arguments) */
+typedef struct {
+  float temperature, draft_temperature;
+} dd_verify_params;
+DD_API size_t dd_verify_draft_workspace(int batch, int total, int vocab);
+DD_API dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int batch,
+                                 int total, int vocab, const void* target_logits,
+                                 int64_t target_stride, const void* draft_logits,
+                                 int64_t draft_stride, const int32_t* draft_tokens,
+                                 const float* draft_conf, const int32_t* cu_draft,
+                                 const float* u_accept, const float* u_sample, int32_t* accepted,
+                                 int32_t* tokens, float* target_prob, void* workspace,
+                                 size_t workspace_bytes, dd_stream_t stream);
+
 /* Clears a whole workspace: the error word and the sampler's state (async on
  * stream).  Call once before a workspace's first use. */
 DD_API dd_status dd_workspace_init(void* workspace, size_t workspace_bytes, dd_stream_t stream);
