@@ -1100,7 +1100,8 @@ dd_status check_cache(const dd_paged_cache* c, bool pointers) {
     return fail(DD_ERR_UNSUPPORTED, "page_size %d (a power of two, 8..512)", c->page_size);
   if (c->head_dim != 64 && c->head_dim != 128)
     return fail(DD_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", c->head_dim);
-  if ((int64_t)c->num_pages * c->heads_kv > INT32_MAX)
+  // (one page past the pool still has a coordinate)
+  if (((int64_t)c->num_pages + 1) * c->heads_kv > INT32_MAX)
     return fail(DD_ERR_UNSUPPORTED, "num_pages * heads_kv exceeds 2^31");
   if (!pointers) return DD_OK;
   if (!c->k || !c->v) return fail(DD_ERR_INVALID_ARG, "NULL cache pointer");

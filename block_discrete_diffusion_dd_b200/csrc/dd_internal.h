@@ -139,6 +139,11 @@ cudaError_t launch_soft_embed(const SoftEmbedArgs& a, cudaStream_t stream);
 bool encode_2d(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t stride,
                int box_inner, int box_outer);
 
+// 3-D TMA map over bf16 elements or bytes: dims in elements, strides of the
+// outer two dimensions in bytes, no swizzling or 128-byte swizzling.
+bool encode_3d(CUtensorMap* m, const void* base, bool bytes, const int64_t (&dims)[3],
+               const int64_t (&strides)[2], const int (&box)[3], bool swizzle128);
+
 // One dense layer on the tensor cores (dd_ffw.cu):
 //   out[r, n] = act(sum_k x[r, k] w[k, n] + bias[n]),  act = GELU or identity
 // x bf16 [rows, K] (row stride K), w bf16 [K, N] (row stride N), bias bf16

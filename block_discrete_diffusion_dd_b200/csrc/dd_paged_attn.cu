@@ -1,114 +1,1117 @@
-// dd_paged_attn.cu -- attention of a chunk of new tokens over a paged cache
-// (dd_paged_attn): new token i of a sequence with n new tokens and `len`
-// tokens in the cache sees the keys j < len - n + i + 1 (causal) or j < len,
-//   O = sum_j softmax_j(scale <q, k_j>) v_j,
-// zeros (log-sum-exp -inf) where it sees none.
+// dd_paged_attn.cu -- attention of new tokens over a paged cache
+// (dd_paged_attn) on the 5th-generation tensor cores: tcgen05.mma with its
+// accumulators in tensor memory, pages gathered by TMA.
 //
-// One warp per (token, query head): lane j scores key j of a block of 32,
-// the warp runs an online softmax in base 2, and each lane accumulates D/32
-// output columns.
+// Definition: new token i of a sequence with n new tokens and `len` tokens in
+// the cache sees the keys j < len - n + i + 1 (causal) or j < len,
+//   O = sum_j softmax_j(scale <q, k_j>) v_j,
+// zeros (log-sum-exp -inf) where it sees none.  The G = Hq / Hkv query heads
+// of a kv head are packed with the new tokens into rows r = i G + h, so that
+// one K/V tile serves them all, whatever G is.
+//
+// Work.  An item is (sequence b, kv head g, kQT query tiles of 128 rows),
+// with the 128-key tiles its last row sees.  Lengths are known on the device
+// only and differ widely, so the items' tiles are laid end to end, each item
+// with kFixed units of overhead in front, and cut into equal shares, one per
+// CTA: every CTA finds its own share from the lengths (a block-wide prefix
+// sum) and walks it.  One wave, no host plan, and the same code serves one
+// token over 65,536 keys and a long chunk.  An item that spans CTAs leaves a
+// partial result per CTA (at most two of a CTA's items are partial: its first
+// and its last), which a second kernel merges in CTA order.
+//
+// Inside a CTA:
+//   warps 0 .. 8 kQT - 1  softmax.  Each owns 16 query rows through the
+//            16-lane tcgen05.ld shape (four threads per row, two shuffles per
+//            row reduction), loads them into the Q tile, runs the online
+//            softmax in fp32 (base 2; O is rescaled only when the running
+//            maximum grows past a margin of 2^8) and writes P back as bf16
+//            where S was, for the P.V product.  Warps without valid rows only
+//            keep the barriers' count.
+//   TMA warp one lane per 8-key group looks the page up; a page's share of the
+//            tile is one box of the tensor map.
+//   MMA warp issues every MMA from one elected lane.  Two S buffers: with two
+//            query tiles one each, in the order PV_0(j) S_0(j+1) PV_1(j)
+//            S_1(j+1); with one query tile (a few rows: decoding) they
+//            alternate, S(j+2) behind PV(j), so that a softmax never waits
+//            for an S product.
+//   convert  (E4M3 cache) expands the 8-bit tiles to bf16 operands: code times
+//            2^e, exact in bf16, so that the products see exactly what the
+//            cache stands for.  The scale bytes follow the page by cp.async.
+// The tensor core runs one thread's MMAs in issue order.  With two query
+// tiles S_q(j) complete therefore means PV_q(j-1) complete, and O may be
+// rescaled; with one, S(j) complete means PV(j-2) complete, and a rescale
+// waits for PV(j-1) on its own barrier.
+//
+// What the cache holds past a sequence's length may be anything, NaN
+// included: masked scores are replaced before they are used, and V rows past
+// the length are set to zero in shared memory, since 0 * NaN is NaN.
+//
+// Every mbarrier wait is bounded in time; on expiry the CTA latches an error,
+// drains its copies and MMAs and frees its tensor memory.
+#include <algorithm>
+#include <mutex>
+
 #include "dd_paged.cuh"
 
 namespace dd {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int BM = 128;  // query rows per tile
+constexpr int BN = 128;  // keys per tile
+constexpr uint32_t kAtom = 128 * 128;  // 128 rows of one 128-byte swizzle atom (64 bf16)
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 2 * BN;    // S buffers first
+constexpr float kLazy = 8.0f;          // log2 units
+constexpr uint64_t kDrainNs = 1000000000ull;
+constexpr int kMaxStages = 6, kMaxRaw = 8;
 
-template <int D, bool kF8>
-__global__ void __launch_bounds__(kWarps * 32)
-    paged_attn_kernel(const PagedBatch p, const PagedPool pool, int Hq,
-                      const __nv_bfloat16* __restrict__ q, int64_t q_stride, float scale2,
-                      int causal, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                      uint32_t* err) {
-  constexpr int DPL = D / 32;
-  __shared__ float sQ[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-  const int t = (int)(unit / Hq), h = (int)(unit % Hq);
-  if (t >= p.total_new) return;
-  const int b = owner_row(p.cu_new, p.batch, t);
-  if (b < 0) return;
-  const ChunkRow c = chunk_row(p, b, err);
-  if (t - c.q0 >= c.n) return;
-  const int seen = causal ? c.len - c.n + (t - c.q0) + 1 : c.len;
-  const int64_t head = (int64_t)(h / (Hq / p.heads_kv)) << p.page_shift;
-  for (int d = lane; d < D; d += 32) sQ[warp][d] = (float)q[t * q_stride + h * D + d];
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[DPL] = {};
-  for (int j0 = 0; j0 < seen; j0 += 32) {
-    const int j = j0 + lane;
-    int64_t row = -1;
-    float s = -INFINITY, fv = 1.f;
-    if (j < seen) {
-      row = pool_row(p, b, j, err);
-      if (row >= 0) {
-        row += head;
-        float x = 0.f;
-        if constexpr (kF8) {
-          const uint8_t* kr = static_cast<const uint8_t*>(pool.k) + row * D;
-          for (int d = 0; d < D; d += 2) {
-            const float2 kd = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(kr + d));
-            x = fmaf(sQ[warp][d], kd.x, fmaf(sQ[warp][d + 1], kd.y, x));
+struct Barriers {
+  uint64_t q_full[2];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t pv_done, mma_final;
+  uint64_t never;  // completed by nothing: the target of the test stall
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D, bool kF8, int kQT>
+struct Lay {
+  static constexpr uint32_t kTile = BM * D * 2;  // a bf16 operand tile
+  static constexpr uint32_t kRaw = BN * D;       // an E4M3 tile
+  static constexpr int kStages = D == 128 ? (kQT == 1 && !kF8 ? 3 : 2) : 4;
+  static constexpr int kRawStages = kF8 ? (kQT == 1 ? 4 : 2) : 0;
+  static constexpr int kSoftWarps = 8 * kQT;
+  static constexpr int kConvWarps = kF8 ? (kQT == 1 ? 8 : 2) : 0;
+  static constexpr int kWarpTMA = kSoftWarps, kWarpMMA = kSoftWarps + 1;
+  static constexpr int kThreads = (kSoftWarps + 2 + kConvWarps) * 32;
+  static constexpr uint32_t kOffK = kQT * kTile;
+  static constexpr uint32_t kOffV = kOffK + kStages * kTile;
+  static constexpr uint32_t kOffRaw = kOffV + kStages * kTile;
+  static constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRaw;
+  static constexpr uint32_t kOffBar = kOffScale + kRawStages * BN;
+  static constexpr uint32_t kSmem = kOffBar + sizeof(Barriers) + 1024;
+  // an item's overhead (its Q tile, first product and epilogue) in key tiles
+  static constexpr int kFixed = kQT == 1 ? 2 : 4;
+  static_assert(kStages <= kMaxStages && kRawStages <= kMaxRaw, "barrier arrays");
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// A partial item that starts in CTA c and ends in CTA `last`: its partials
+// are slot 1 of CTA c and slot 0 of CTAs c + 1 .. last.
+struct Split {
+  int b, g, tp, last;  // b < 0: none starts here
+};
+
+struct Params {
+  PagedBatch b;
+  const uint8_t *k_scale, *v_scale;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int Hq, G, causal, max_ctas;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  Split* split;       // [max_ctas]
+  int slot_rows;      // rows kept per slot
+  uint32_t* part_o;   // [2 max_ctas][slot_rows][D / 2]: O / l as fp16 pairs times 2^-e_row
+  float2* part_lse;   // [2 max_ctas][slot_rows]: log2-domain LSE, 2^e_row
+  uint32_t* err;
+  uint64_t wait_ns;
+  int stall;
+};
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ int row_exponent(float m) {
+  if (!(m > 0.f) || !(m <= 3.4e38f)) return 0;
+  return min(113, max(-126, ilogbf(m) - 14));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Query-tile groups of a sequence, and the key tiles of group tp.
+template <int kQT>
+__device__ __forceinline__ int tile_groups(const ChunkRow& r, int G) {
+  return cdiv(r.n * G, kQT * BM);
+}
+template <int kQT>
+__device__ __forceinline__ int key_tiles(const ChunkRow& r, int G, int causal, int tp) {
+  const int last = (min((tp + 1) * kQT * BM, r.n * G) - 1) / G;  // last token of the group
+  const int seen = causal ? r.len - r.n + last + 1 : r.len;
+  return cdiv(max(seen, 0), BN);
+}
+
+// One CTA's part of an item.
+struct Seg {
+  int b, g, tp;
+  ChunkRow r;
+  int t0, t1, nt;  // key tiles [t0, t1) of nt
+};
+
+// Walks a CTA's share [pos, end) of the items laid end to end.
+template <int kQT, int kFixed>
+struct Walk {
+  int64_t pos, end;
+  int b, g, tp, x;  // the item, and the place in it
+  ChunkRow r;
+  int groups;
+
+  __device__ __forceinline__ void load(const Params& p) {
+    r = chunk_row(p.b, b, p.err);
+    groups = tile_groups<kQT>(r, p.G);
+  }
+  __device__ __forceinline__ bool next(const Params& p, Seg& s) {
+    while (pos < end) {
+      while (groups == 0) {  // a sequence without new tokens
+        ++b;
+        load(p);
+      }
+      const int nt = key_tiles<kQT>(r, p.G, p.causal, tp);
+      const int w = nt + kFixed;
+      const int x1 = (int)min((int64_t)w, x + (end - pos));
+      s.b = b;
+      s.g = g;
+      s.tp = tp;
+      s.r = r;
+      s.nt = nt;
+      s.t0 = max(0, x - kFixed);
+      s.t1 = max(0, x1 - kFixed);
+      const bool some = s.t1 > s.t0 || (nt == 0 && x == 0);
+      pos += x1 - x;
+      x = x1;
+      if (x == w) {
+        x = 0;
+        if (++tp == groups) {
+          tp = 0;
+          if (++g == p.b.heads_kv) {
+            g = 0;
+            ++b;
+            if (pos < end) load(p);
           }
-          x *= pow2f((int)pool.k_scale[row] - 127);
-          fv = pow2f((int)pool.v_scale[row] - 127);
-        } else {
-          const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(pool.k) + row * D;
-          for (int d = 0; d < D; ++d) x = fmaf(sQ[warp][d], (float)kr[d], x);
         }
-        s = x * scale2;
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+};
+
+// The share of this CTA: a block-wide prefix sum over the sequences.
+struct Share {
+  int64_t pos, end, total;
+  int ctas, b, g, tp, x;
+};
+
+template <int D, bool kF8, int kQT>
+__device__ int64_t seq_weight(const Params& p, int b) {
+  using L = Lay<D, kF8, kQT>;
+  const ChunkRow r = chunk_row(p.b, b, p.err);
+  const int groups = tile_groups<kQT>(r, p.G);
+  int64_t w = 0;
+  for (int tp = 0; tp < groups; ++tp) w += key_tiles<kQT>(r, p.G, p.causal, tp) + L::kFixed;
+  return w * p.b.heads_kv;
+}
+
+template <int D, bool kF8, int kQT>
+__device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
+  using L = Lay<D, kF8, kQT>;
+  constexpr int kT = L::kThreads, kW = kT / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // exclusive prefix of v over the block; *all gets the block's sum
+  auto scan = [&](int64_t v, int64_t* all) {
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int64_t before = 0, sum = 0;
+    for (int i = 0; i < kW; ++i) {
+      if (i < warp) before += warp_sums[i];
+      sum += warp_sums[i];
+    }
+    __syncthreads();
+    *all = sum;
+    return before + inc - v;
+  };
+  int64_t total = 0, w = 0, at = 0, all;
+  for (int b0 = 0; b0 < p.b.batch; b0 += kT) {
+    const int b = b0 + threadIdx.x;
+    w = b < p.b.batch ? seq_weight<D, kF8, kQT>(p, b) : 0;
+    at = scan(w, &all);
+    total += all;
+  }
+  // no CTA takes less than one item's overhead and as many tiles again
+  const int64_t most = (total + 2 * L::kFixed - 1) / (2 * L::kFixed);
+  const int ctas = (int)min((int64_t)gridDim.x, most);
+  const int64_t pos = ctas > 0 && blockIdx.x < ctas ? blockIdx.x * total / ctas : 0;
+  const int64_t end = ctas > 0 && blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : 0;
+  if (threadIdx.x == 0) {
+    sh->total = total;
+    sh->ctas = ctas;
+    sh->pos = pos;
+    sh->end = end;
+  }
+  if (end > pos) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.b.batch; b0 += kT) {
+      const int b = b0 + threadIdx.x;
+      if (p.b.batch > kT) {  // (a single round keeps its w and prefix)
+        w = b < p.b.batch ? seq_weight<D, kF8, kQT>(p, b) : 0;
+        at = scan(w, &all);
+      }
+      if (pos >= base + at && pos < base + at + w) {
+        int64_t off = pos - base - at;
+        const ChunkRow r = chunk_row(p.b, b, p.err);
+        const int64_t head = w / p.b.heads_kv;
+        sh->b = b;
+        sh->g = (int)(off / head);
+        off %= head;
+        int tp = 0;
+        while (true) {
+          const int wi = key_tiles<kQT>(r, p.G, p.causal, tp) + L::kFixed;
+          if (off < wi) break;
+          off -= wi;
+          ++tp;
+        }
+        sh->tp = tp;
+        sh->x = (int)off;
+      }
+      base += all;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t off) {
+  return base + (uint64_t)(off >> 4);
+}
+
+// S = Q K^T: K-major operands, 16 elements (32 bytes) per MMA through the
+// 128-byte swizzle atoms.
+template <int D>
+__device__ __forceinline__ void issue_s(uint32_t dS, uint64_t aq, uint64_t bk) {
+  constexpr uint32_t id = idesc_bf16_f32(BM, BN, 0, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * kAtom + (kk & 3) * 32;
+    tc_mma_ss(dS, desc_at(aq, off), desc_at(bk, off), id, kk > 0);
+  }
+}
+// O (+)= P V: P from tensor memory, two keys per column; V MN-major.
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t dO, uint32_t aP, uint64_t bv, bool acc) {
+  constexpr uint32_t id = idesc_bf16_f32(BM, D, 0, 1);
+#pragma unroll
+  for (int kk = 0; kk < BN / 16; ++kk)
+    tc_mma_ts(dO, aP + (uint32_t)(kk * 8), desc_at(bv, kk * 16 * 128), id,
+              (acc || kk > 0) ? 1u : 0u);
+}
+
+// 16 E4M3 codes (16 bytes) times f as bf16.
+__device__ __forceinline__ void expand16(uint4 c, float f, uint4& lo, uint4& hi) {
+  const float2 ff = make_float2(f, f);
+  auto pair = [&](uint32_t w) {
+    const float2 x = __fmul2_rn(e4m3x2_to_float2(w), ff);
+    return pack_bf16x2(x.x, x.y);
+  };
+  lo = make_uint4(pair(c.x), pair(c.x >> 16), pair(c.y), pair(c.y >> 16));
+  hi = make_uint4(pair(c.z), pair(c.z >> 16), pair(c.w), pair(c.w >> 16));
+}
+
+template <int D, bool kF8, int kQT>
+__global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const Params p) {
+  using L = Lay<D, kF8, kQT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Share share;
+  __shared__ int64_t warp_sums[L::kThreads / 32];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Barriers* bars = reinterpret_cast<Barriers*>(smem + L::kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&bars->k_full[i], kF8 ? L::kConvWarps : 1);
+      mbar_init(&bars->v_full[i], kF8 ? L::kConvWarps : 1);
+      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->v_empty[i], 1);
+    }
+    for (int i = 0; i < L::kRawStages; ++i) {
+      mbar_init(&bars->raw_full[i], 1 + BN / 8);  // the pages, and each lane's scale bytes
+      mbar_init(&bars->raw_empty[i], L::kConvWarps);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&bars->q_full[q], 8);
+      mbar_init(&bars->s_full[q], 1);
+      mbar_init(&bars->p_full[q], 8);
+      mbar_init(&bars->o_done[q], 1);
+    }
+    mbar_init(&bars->pv_done, 1);
+    mbar_init(&bars->mma_final, 1);
+    mbar_init(&bars->never, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == L::kWarpMMA) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  find_share<D, kF8, kQT>(p, &share, warp_sums);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  Walk<kQT, L::kFixed> walk;
+  walk.pos = share.pos;
+  walk.end = share.end;
+  const bool work = walk.pos < walk.end;
+  walk.b = share.b;
+  walk.g = share.g;
+  walk.tp = share.tp;
+  walk.x = share.x;
+  if (work) walk.load(p);
+  Seg sg;
+
+  if (warp == L::kWarpTMA) {
+    // ------------------------------------------------------------ TMA
+    // Lane l < 16 looks up the page of the tile's 8-key group l, and issues
+    // the copy where that group starts a page (or the tile).
+    int tile = 0;  // tiles issued
+    const int ps = 1 << p.b.page_shift, per = min(ps, BN);
+    if (lane == 0 && work) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+    }
+    bool ok = true;
+    while (ok && walk.next(p, sg)) {
+      const int32_t* table = p.b.page_table + (int64_t)sg.b * p.b.max_pages;
+      auto look = [&](int t) {
+        const int pos = t * BN + lane * 8;
+        return lane < BN / 8 && t < sg.t1 && pos < sg.r.len
+                   ? __ldg(table + (pos >> p.b.page_shift)) : -1;
+      };
+      int page = look(sg.t0);
+      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++tile) {
+        const int after = look(t + 1);
+        const int pos = t * BN + lane * 8;
+        const bool live = lane < BN / 8 && pos < sg.r.len;
+        int at = page;
+        if (live && (uint32_t)page >= (uint32_t)p.b.num_pages) {
+          atomicOr(p.err, kDevErrBounds);
+          at = p.b.num_pages;  // outside the tensor map: read as zero
+        }
+        const bool lead = live && (lane * 8) % per == 0;
+        const uint32_t bytes =
+            (uint32_t)__popc(__ballot_sync(0xffffffffu, lead)) * per * D * (kF8 ? 1 : 2);
+        const int c1 = pos & (ps - 1) & ~(per - 1), c2 = at * p.b.heads_kv + sg.g;
+        for (int v = 0; v < 2 && ok; ++v) {
+          const CUtensorMap* map = v ? &tmV : &tmK;
+          uint64_t *full, *empty;
+          uint8_t* dst;
+          int round;
+          if constexpr (kF8) {
+            const int n = 2 * tile + v, st = n % L::kRawStages;
+            round = n / L::kRawStages;
+            full = &bars->raw_full[st];
+            empty = &bars->raw_empty[st];
+            dst = smem + L::kOffRaw + st * L::kRaw;
+          } else {
+            const int st = tile % L::kStages;
+            round = tile / L::kStages;
+            full = v ? &bars->v_full[st] : &bars->k_full[st];
+            empty = v ? &bars->v_empty[st] : &bars->k_empty[st];
+            dst = smem + (v ? L::kOffV : L::kOffK) + st * L::kTile;
+          }
+          if (round > 0)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded(empty, (round - 1) & 1, abort_flag, p.wait_ns));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          if constexpr (kF8) {
+            if (lead) tma_load_3d(dst + lane * 8 * D, map, full, 0, c1, c2);
+            if (lane < BN / 8) {
+              if (live && at == page) {
+                const int64_t row = ((int64_t)c2 << p.b.page_shift) + (pos & (ps - 1));
+                uint8_t* sc = smem + L::kOffScale + ((2 * tile + v) % L::kRawStages) * BN;
+                cp_async8(sc + lane * 8, (v ? p.v_scale : p.k_scale) + row);
+              }
+              cp_async_arrive(full);
+            }
+          } else if (lead) {
+#pragma unroll
+            for (int a = 0; a < D / 64; ++a)
+              tma_load_3d(dst + a * kAtom + lane * 8 * 128, map, full, a * 64, c1, c2);
+          }
+          __syncwarp();
+        }
+        page = after;
       }
     }
-    float mx = s;
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = ex2_approx(m - ref), pr = ex2_approx(s - ref);
-    float ps = pr;
-    for (int off = 16; off > 0; off >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, off);
-    l = l * alpha + ps;
-    m = mn;
-    for (int k = 0; k < DPL; ++k) o[k] *= alpha;
-    for (int jj = 0; jj < 32; ++jj) {
-      const float w = __shfl_sync(0xffffffffu, pr * fv, jj);
-      const int64_t r = __shfl_sync(0xffffffffu, row, jj);
-      if (r < 0) continue;
-      for (int k = 0; k < DPL; ++k) {
-        const int64_t at = r * D + lane + 32 * k;
-        float x;
-        if constexpr (kF8)
-          x = e4m3x2_to_float2(static_cast<const uint8_t*>(pool.v)[at]).x;
-        else
-          x = (float)static_cast<const __nv_bfloat16*>(pool.v)[at];
-        o[k] = fmaf(w, x, o[k]);
+    // copies still in flight must land before the CTA exits (all have, unless
+    // the CTA gave up: then the last tiles' barriers are waited for, those of
+    // copies that were not issued any more running out)
+    if (*abort_flag) {
+      for (int n = max(0, tile - kMaxStages); n <= tile; ++n)
+        for (int v = 0; v < 2; ++v) {
+          const int i = 2 * n + v;
+          uint64_t* full = kF8 ? &bars->raw_full[i % max(1, L::kRawStages)]
+                           : v ? &bars->v_full[n % L::kStages] : &bars->k_full[n % L::kStages];
+          const int round = kF8 ? i / max(1, L::kRawStages) : n / L::kStages;
+          mbar_wait_bounded(full, round & 1, nullptr, kDrainNs / 64);
+        }
+    }
+    __syncwarp();
+  } else if (warp == L::kWarpMMA) {
+    // ------------------------------------------------------------ MMA
+    const bool leader = elect_one_sync();
+    const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t dK = smem_desc_sw128(smem_u32(smem + L::kOffK), 16, 1024);
+    const uint64_t dV = smem_desc_sw128(smem_u32(smem + L::kOffV), kAtom, 1024);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool r = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns));
+      tc_fence_after();
+      return r;
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (leader) tc_commit(bar);
+      __syncwarp();
+    };
+    int kt = 0, vt = 0;             // K and V tiles consumed
+    int pcnt[2] = {0, 0};           // P tiles consumed per buffer
+    int segs[2] = {0, 0};           // segments per query tile
+    int sbuf = 0, pbuf = 0;         // kQT = 1: the next S / P buffer
+    bool ok = true, first = true;
+    // S of key tile kt for query tile q (all of them share the K stage)
+    auto s_tile = [&](int nq) {
+      const int st = kt % L::kStages;
+      if (!wait(&bars->k_full[st], (kt / L::kStages) & 1)) return false;
+      for (int q = 0; q < nq; ++q) {
+        const int buf = kQT == 1 ? sbuf : q;
+        if (leader) {
+          issue_s<D>(tmem + buf * BN, desc_at(dQ, q * L::kTile), desc_at(dK, st * L::kTile));
+          tc_commit(&bars->s_full[buf]);
+        }
+        __syncwarp();
+      }
+      sbuf ^= 1;
+      commit(&bars->k_empty[st]);
+      ++kt;
+      return true;
+    };
+    while (ok && walk.next(p, sg)) {
+      const int n = sg.t1 - sg.t0;
+      if (n == 0) continue;
+      const int rows = sg.r.n * p.G - sg.tp * kQT * BM;
+      const int nq = kQT == 1 ? 1 : min(kQT, cdiv(rows, BM));
+      for (int q = 0; q < nq && ok; ++q) ok = wait(&bars->q_full[q], segs[q] & 1);
+      if (!ok) break;
+      // the first products
+      if (!(ok = s_tile(nq))) break;
+      if (kQT == 1 && n > 1 && !(ok = s_tile(1))) break;
+      if (first && p.stall && !(ok = wait(&bars->never, 0))) break;
+      first = false;
+      for (int j = 0; j < n && ok; ++j) {
+        const int vst = vt % L::kStages;
+        if (!(ok = wait(&bars->v_full[vst], (vt / L::kStages) & 1))) break;
+        if constexpr (!kF8) {
+          // V rows past the sequence's length: zero, whatever the page holds
+          const int valid = sg.r.len - (sg.t0 + j) * BN;
+          if (valid < BN) {
+            uint8_t* v = smem + L::kOffV + vst * L::kTile;
+            for (int i = lane; i < (BN - valid) * 8; i += 32)
+#pragma unroll
+              for (int a = 0; a < D / 64; ++a)
+                *reinterpret_cast<uint4*>(v + a * kAtom + valid * 128 + i * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        const uint64_t bv = desc_at(dV, vst * L::kTile);
+        // the next product: tile j + 1 for two query tiles (interleaved with
+        // the P.V products), tile j + 2 for one
+        const bool more = j + (kQT == 1 ? 2 : 1) < n;
+        const int kst = kt % L::kStages;
+        for (int q = 0; q < nq; ++q) {
+          const int buf = kQT == 1 ? pbuf : q;
+          if (!(ok = wait(&bars->p_full[buf], pcnt[buf] & 1))) break;
+          ++pcnt[buf];
+          if (leader)
+            issue_pv<D>(tmem + kTmemO + q * D, tmem + buf * BN, bv, j > 0);
+          __syncwarp();
+          if (kQT == 1) {
+            commit(&bars->pv_done);
+          } else if (more) {
+            if (q == 0 && !(ok = wait(&bars->k_full[kst], (kt / L::kStages) & 1))) break;
+            if (leader) {
+              issue_s<D>(tmem + q * BN, desc_at(dQ, q * L::kTile), desc_at(dK, kst * L::kTile));
+              tc_commit(&bars->s_full[q]);
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+        pbuf ^= 1;
+        commit(&bars->v_empty[vst]);
+        ++vt;
+        if (more) {
+          if (kQT == 1) {
+            if (!(ok = s_tile(1))) break;
+          } else {
+            commit(&bars->k_empty[kst]);
+            ++kt;
+          }
+        }
+      }
+      if (!ok) break;
+      for (int q = 0; q < nq; ++q) {
+        commit(&bars->o_done[q]);
+        ++segs[q];
+      }
+    }
+    // every MMA issued above has completed before TMEM is released
+    commit(&bars->mma_final);
+    mbar_wait_bounded(&bars->mma_final, 0, nullptr, kDrainNs);
+    __syncwarp();
+  } else if (warp < L::kSoftWarps) {
+    // ------------------------------------------------------------ softmax
+    const int q = warp >> 3, wl = warp & 3, hv = (warp >> 2) & 1;
+    const int t4 = lane & 3;
+    const int rbase = wl * 32 + hv * 16;
+    const int rA = rbase + (lane >> 2), rB = rA + 8;  // query rows in tile q
+    const uint32_t lane_base = (uint32_t)rbase << 16;
+    const uint32_t tO = tmem + lane_base + kTmemO + (uint32_t)(q * D);
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+    uint8_t* tileQ = smem + q * L::kTile;
+    int cnt = 0, seg = 0;  // tiles and segments of this query tile
+    bool ok = true;
+    auto quad_max = [](float v) {
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+      return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+    };
+    auto quad_sum = [](float v) {
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      return v + __shfl_xor_sync(0xffffffffu, v, 2);
+    };
+    while (ok && walk.next(p, sg)) {
+      const int row0 = (sg.tp * kQT + q) * BM;         // packed row of the tile's row 0
+      const int rows = sg.r.n * p.G - row0;            // valid rows of this tile
+      if (rows <= 0) continue;
+      const bool active = rbase < rows;
+      const int first_head = sg.g * p.G;
+      // global row (token, head) of the tile's row r, in elements of q / out
+      auto token = [&](int r, int& head) {
+        const int pr = row0 + r, i = pr / p.G;
+        head = first_head + pr - i * p.G;
+        return sg.r.q0 + i;
+      };
+      if (sg.nt == 0) {  // nothing to see: zeros
+        for (int r = rbase + lane / kChunks; r < rbase + 16; r += 32 / kChunks)
+          if (r < rows) {
+            int h;
+            const int64_t at = (int64_t)token(r, h) * p.Hq + h;
+            reinterpret_cast<uint4*>(p.out + at * D)[lane % kChunks] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse && lane % kChunks == 0) p.lse[at] = -INFINITY;
+          }
+        continue;
+      }
+      if (active) {  // this warp's 16 rows of Q, into the K-major swizzled tile
+        uint4 v[16 * kChunks / 32];
+#pragma unroll
+        for (int i = 0; i < 16 * kChunks / 32; ++i) {
+          const int r = rbase + i * (32 / kChunks) + lane / kChunks;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) {
+            int h;
+            const int64_t t = token(r, h);
+            v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (int64_t)h * D) +
+                         lane % kChunks);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16 * kChunks / 32; ++i) {
+          const int r = rbase + i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+          *reinterpret_cast<uint4*>(tileQ + (c >> 3) * kAtom + r * 128 +
+                                    (((c & 7) ^ (r & 7)) << 4)) = v[i];
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full[q]);
+      // keys seen by rows A and B, and the fewest of the warp's rows
+      auto limit = [&](int r) {
+        if (r >= rows) return 0;
+        const int i = (row0 + r) / p.G;
+        return p.causal ? sg.r.len - sg.r.n + i + 1 : sg.r.len;
+      };
+      const int limA = limit(rA), limB = limit(rB), lim0 = limit(rbase);
+      const int full_to = rbase + 16 <= rows ? lim0 : 0;
+      float mrefA = -1e30f, mrefB = -1e30f, lA = 0.f, lB = 0.f;
+      const int n = sg.t1 - sg.t0;
+      for (int j = 0; j < n; ++j, ++cnt) {
+        const int buf = kQT == 1 ? cnt & 1 : q;
+        const uint32_t par = (kQT == 1 ? cnt >> 1 : cnt) & 1;
+        const uint32_t tS = tmem + lane_base + (uint32_t)(buf * BN);
+        // wait outcomes are made warp-uniform: tcgen05.ld/st are .sync.aligned
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_bounded(&bars->s_full[buf], par, abort_flag, p.wait_ns))) {
+          ok = false;
+          break;
+        }
+        if (active) {
+          tc_fence_after();
+          const int k0 = (sg.t0 + j) * BN;
+          uint32_t sv[64];
+          tmem_ld16x256b_x16(tS, sv);
+          if (k0 + BN > full_to) {
+            const int vA = limA - k0, vB = limB - k0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int c = 8 * i + 2 * t4;
+              if (c >= vA) sv[4 * i] = __float_as_uint(-INFINITY);
+              if (c + 1 >= vA) sv[4 * i + 1] = __float_as_uint(-INFINITY);
+              if (c >= vB) sv[4 * i + 2] = __float_as_uint(-INFINITY);
+              if (c + 1 >= vB) sv[4 * i + 3] = __float_as_uint(-INFINITY);
+            }
+          }
+          float ma = fmaxf(__uint_as_float(sv[0]), __uint_as_float(sv[1]));
+          float mb = fmaxf(__uint_as_float(sv[2]), __uint_as_float(sv[3]));
+#pragma unroll
+          for (int i = 1; i < 16; ++i) {
+            ma = fmaxf(ma, fmaxf(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])));
+            mb = fmaxf(mb, fmaxf(__uint_as_float(sv[4 * i + 2]), __uint_as_float(sv[4 * i + 3])));
+          }
+          const float xa = quad_max(ma) * p.scale_log2, xb = quad_max(mb) * p.scale_log2;
+          if (j == 0) {
+            // the reference is the row's maximum (a row that sees none of
+            // this tile keeps a finite one: its exponentials are 0)
+            mrefA = fmaxf(mrefA, xa);
+            mrefB = fmaxf(mrefB, xb);
+          } else if (__any_sync(0xffffffffu, xa > mrefA + kLazy || xb > mrefB + kLazy)) {
+            // rescale (rare, a warp-uniform decision); the last P.V product
+            // has to be complete
+            if (kQT == 1 &&
+                !__all_sync(0xffffffffu, mbar_wait_bounded(&bars->pv_done, (cnt - 1) & 1,
+                                                           abort_flag, p.wait_ns))) {
+              ok = false;
+              break;
+            }
+            if (kQT == 1) tc_fence_after();
+            const float na = fmaxf(mrefA, xa), nb = fmaxf(mrefB, xb);
+            const float alA = ex2_approx(mrefA - na), alB = ex2_approx(mrefB - nb);
+            lA *= alA;
+            lB *= alB;
+#pragma unroll 1
+            for (int c16 = 0; c16 < D / 16; ++c16) {
+              uint32_t o[8];
+              tmem_ld16x256b_x2(tO + (uint32_t)(c16 * 16), o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * ((e & 2) ? alB : alA));
+              tmem_st16x256b_x2(tO + (uint32_t)(c16 * 16), o);
+            }
+            mrefA = na;
+            mrefB = nb;
+          }
+          const float2 na = make_float2(-mrefA, -mrefA), nb = make_float2(-mrefB, -mrefB);
+          float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
+          uint32_t w[32];  // 16x128b: w[2i] row A, w[2i + 1] row B, column 4 i + t % 4
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 da = __ffma2_rn(
+                make_float2(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])), sl2, na);
+            const float2 db = __ffma2_rn(
+                make_float2(__uint_as_float(sv[4 * i + 2]), __uint_as_float(sv[4 * i + 3])), sl2,
+                nb);
+            const float2 pa = make_float2(ex2_approx(da.x), ex2_approx(da.y));
+            const float2 pb = make_float2(ex2_approx(db.x), ex2_approx(db.y));
+            sa = __fadd2_rn(sa, pa);
+            sb = __fadd2_rn(sb, pb);
+            w[2 * i] = pack_bf16x2(pa.x, pa.y);
+            w[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
+          }
+          tmem_st16x128b_x16(tS, w);
+          lA += sa.x + sa.y;
+          lB += sb.x + sb.y;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[buf]);
+      }
+      if (!ok) break;
+      // epilogue: O / l and the log-sum-exp
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_bounded(&bars->o_done[q], seg & 1, abort_flag, p.wait_ns))) {
+        ok = false;
+        break;
+      }
+      ++seg;
+      if (!active) continue;
+      tc_fence_after();
+      const float lrowA = quad_sum(lA), lrowB = quad_sum(lB);
+      const float invA = lrowA > 0.f ? 1.f / lrowA : 0.f, invB = lrowB > 0.f ? 1.f / lrowB : 0.f;
+      const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (sg.t0 > 0 ? 0 : 1);
+      uint32_t o[D / 2];
+      if constexpr (D == 128) tmem_ld16x256b_x16(tO, o);
+      else tmem_ld16x256b_x8(tO, o);
+      float sA = invA, sB = invB;
+      int eA = 0, eB = 0;
+      if (!whole) {
+        // fp16 pairs, each row scaled by a power of two that puts its largest
+        // magnitude in [2^14, 2^15): 11 significant bits against the row's
+        // maximum in half the bytes of fp32
+        float mA = 0.f, mB = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          mA = fmaxf(mA, fmaxf(fabsf(__uint_as_float(o[4 * i])), fabsf(__uint_as_float(o[4 * i + 1]))));
+          mB = fmaxf(mB, fmaxf(fabsf(__uint_as_float(o[4 * i + 2])),
+                               fabsf(__uint_as_float(o[4 * i + 3]))));
+        }
+        eA = row_exponent(quad_max(mA) * invA);
+        eB = row_exponent(quad_max(mB) * invB);
+        sA = invA * pow2f(-eA);
+        sB = invB * pow2f(-eB);
+      }
+      // staged in this warp's own rows of the Q tile (whose products are
+      // complete), in the Q tile's swizzled layout: a store hits 32 banks
+      auto piece = [&](int r, int c) {
+        return tileQ + (c >> 3) * kAtom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      };
+      auto put = [&](int r, int i, float x, float y, float s) {
+        reinterpret_cast<uint32_t*>(piece(r, i))[t4] =
+            whole ? pack_bf16x2(x * s, y * s) : pack_f16x2(x * s, y * s);
+      };
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        put(rA, i, __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), sA);
+        put(rB, i, __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]), sB);
+      }
+      if (t4 == 0) {
+        const float lseA = lrowA > 0.f ? mrefA + __log2f(lrowA) : -INFINITY;
+        const float lseB = lrowB > 0.f ? mrefB + __log2f(lrowB) : -INFINITY;
+        auto put_lse = [&](int r, float l, int e) {
+          if (r >= rows) return;
+          if (whole) {
+            int h;
+            const int64_t t = token(r, h);
+            if (p.lse) p.lse[t * p.Hq + h] = l * 0.6931471805599453f;
+          } else {
+            p.part_lse[slot * p.slot_rows + q * BM + r] = make_float2(l, pow2f(e));
+          }
+        };
+        put_lse(rA, lseA, eA);
+        put_lse(rB, lseB, eB);
+      }
+      __syncwarp();
+      for (int r = rbase + lane / kChunks; r < rbase + 16; r += 32 / kChunks) {
+        if (r >= rows) break;
+        const int c = lane % kChunks;
+        const uint4 v = *reinterpret_cast<const uint4*>(piece(r, c));
+        if (whole) {
+          int h;
+          const int64_t t = token(r, h);
+          reinterpret_cast<uint4*>(p.out + (t * p.Hq + h) * D)[c] = v;
+        } else {
+          reinterpret_cast<uint4*>(p.part_o + (slot * p.slot_rows + q * BM + r) * (D / 2))[c] = v;
+        }
+      }
+      __syncwarp();
+    }
+  } else if constexpr (kF8) {
+    // ------------------------------------------------------------ convert
+    // A group of 8 lanes takes two rows, four 16-byte pieces of each; the
+    // rows are paired (r, r ^ 5) at D = 128 and (r, r + 1) at D = 64 so that
+    // both the reads of the 8-bit tile and the writes of the bf16 tile, each
+    // swizzled by its row, touch every bank once.
+    const int cw = warp - L::kWarpMMA - 1;
+    const int oct = lane >> 3, sel = (lane >> 2) & 1, kk = lane & 3;
+    const int sub = D == 128 ? (sel ? oct ^ 5 : oct) : 2 * oct + sel;  // row in its group of 8
+    int tile = 0;
+    bool ok = true;
+    while (ok && walk.next(p, sg)) {
+      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++tile) {
+        const int valid = sg.r.len - t * BN;
+        for (int v = 0; v < 2; ++v) {
+          const int n = 2 * tile + v, rs = n % L::kRawStages, st = tile % L::kStages;
+          uint64_t* empty = v ? &bars->v_empty[st] : &bars->k_empty[st];
+          uint64_t* full = v ? &bars->v_full[st] : &bars->k_full[st];
+          ok = mbar_wait_bounded(&bars->raw_full[rs], (n / L::kRawStages) & 1, abort_flag,
+                                 p.wait_ns);
+          if (ok && tile >= L::kStages)
+            ok = mbar_wait_bounded(empty, (tile / L::kStages - 1) & 1, abort_flag, p.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* raw = smem + L::kOffRaw + rs * L::kRaw;
+          const uint8_t* sc = smem + L::kOffScale + rs * BN;
+          uint8_t* dst = smem + (v ? L::kOffV : L::kOffK) + st * L::kTile;
+#pragma unroll 2
+          for (int grp = cw; grp < BN / 8; grp += L::kConvWarps) {
+            const int r = grp * 8 + sub;
+            const float f = pow2f((int)sc[r] - 127);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+              const int c = kk + 4 * half;
+              const uint8_t* src = D == 128 ? raw + r * 128 + ((c ^ sub) << 4) : raw + r * 64 + (c << 4);
+              uint4 lo, hi;
+              expand16(*reinterpret_cast<const uint4*>(src), f, lo, hi);
+              if (r >= valid) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+              uint8_t* d = dst + half * kAtom + r * 128;
+              *reinterpret_cast<uint4*>(d + (((2 * kk) ^ sub) << 4)) = lo;
+              *reinterpret_cast<uint4*>(d + (((2 * kk + 1) ^ sub) << 4)) = hi;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->raw_empty[rs]);
+            mbar_arrive(full);
+          }
+        }
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int64_t at = (int64_t)t * Hq + h;
-  for (int k = 0; k < DPL; ++k) out[at * D + lane + 32 * k] = (__nv_bfloat16)(o[k] * inv);
-  if (lse && lane == 0)
-    lse[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+
+  if (threadIdx.x == 0) {
+    // the item that starts in this CTA's share and ends in a later one
+    Split s{-1, 0, 0, 0};
+    Walk<kQT, L::kFixed> w;
+    w.pos = share.pos;
+    w.end = share.end;
+    if (blockIdx.x < share.ctas && w.pos < w.end) {
+      w.b = share.b;
+      w.g = share.g;
+      w.tp = share.tp;
+      w.x = share.x;
+      w.load(p);
+      Seg e;
+      while (w.next(p, e))
+        if (e.t0 == 0 && e.t1 < e.nt && e.t1 > 0) {
+          // its last unit, and the CTA whose share holds it
+          const int64_t last = share.end + (e.nt - e.t1) - 1;
+          int c = (int)(last * share.ctas / share.total);
+          while ((c + 1) * share.total / share.ctas <= last) ++c;
+          while (c * share.total / share.ctas > last) --c;
+          s = Split{e.b, e.g, e.tp, c};
+        }
+    }
+    p.split[blockIdx.x] = s;
+  }
+  if (*abort_flag && threadIdx.x == 0) atomicOr(p.err, kDevErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == L::kWarpMMA) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kF8>
-cudaError_t launch_t(const PagedAttnArgs& a, cudaStream_t stream) {
-  const int64_t units = (int64_t)a.p.total_new * a.heads_q;
-  paged_attn_kernel<D, kF8><<<(unsigned)((units + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
-      a.p, a.pool, a.heads_q, static_cast<const __nv_bfloat16*>(a.q), a.q_stride,
-      a.scale * 1.4426950408889634f, a.causal ? 1 : 0, static_cast<__nv_bfloat16*>(a.out), a.lse,
-      a.err);
-  note_launch();
-  return cudaGetLastError();
+// Merges an item's partials: lse = log2 sum 2^lse_s, O = sum_s 2^(lse_s - lse)
+// 2^e_s O_s.  Block (c, part) takes kMergeRows rows of the item that starts in
+// CTA c; a warp takes one row at a time, lane s the weight of split s and
+// lane l the columns (D / 32) l ..
+constexpr int kMergeWarps = 8, kMergeRows = 16;
+
+template <int D, int kQT>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Params p) {
+  constexpr int kC = D / 64;  // fp16 pairs per lane
+  pdl_wait();
+  pdl_trigger();
+  const int parts = cdiv(p.slot_rows, kMergeRows);
+  const int c = blockIdx.x / parts, part = blockIdx.x % parts;
+  const Split s = p.split[c];
+  if (s.b < 0) return;
+  const ChunkRow r = chunk_row(p.b, s.b, p.err);
+  const int row0 = s.tp * kQT * BM, rows = min(r.n * p.G - row0, p.slot_rows);
+  const int ns = s.last - c + 1;
+  if (ns < 1 || s.last >= p.max_ctas) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = warp; i < kMergeRows; i += kMergeWarps) {
+    const int row = part * kMergeRows + i;
+    if (row >= rows) break;
+    auto at = [&](int k) {  // row of split k
+      return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.slot_rows + row;
+    };
+    float mx = -INFINITY;
+    for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, __ldcg(&p.part_lse[at(k)]).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = fmaxf(mx, -1e30f);
+    float wsum = 0.f, acc[2 * kC] = {};
+    for (int k0 = 0; k0 < ns; k0 += 32) {
+      const int k = k0 + lane;
+      const float2 ls = k < ns ? __ldcg(&p.part_lse[at(k)]) : make_float2(-INFINITY, 0.f);
+      const float w = exp2f(ls.x - ref), wo = w * ls.y;
+      wsum += w;
+      const int n = min(32, ns - k0);
+      for (int j0 = 0; j0 < n; j0 += 8) {
+        uint32_t ov[8][kC];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (j0 + u < n) {
+            const uint32_t* src = p.part_o + at(k0 + j0 + u) * (D / 2) + lane * kC;
+            if constexpr (kC == 2) {
+              const uint2 x = __ldcg(reinterpret_cast<const uint2*>(src));
+              ov[u][0] = x.x;
+              ov[u][1] = x.y;
+            } else {
+              ov[u][0] = __ldcg(src);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kC; ++e) ov[u][e] = 0;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, wo, j0 + u);
+#pragma unroll
+          for (int e = 0; e < kC; ++e) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&ov[u][e]));
+            acc[2 * e] = fmaf(wu, x.x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(wu, x.y, acc[2 * e + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const int pr = row0 + row, tok = pr / p.G;
+    const int64_t orow = (int64_t)(r.q0 + tok) * p.Hq + s.g * p.G + pr - tok * p.G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * kC;
+#pragma unroll
+    for (int e = 0; e < kC; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (p.lse && lane == 0)
+      p.lse[orow] = wsum > 0.f ? (ref + __log2f(wsum)) * 0.6931471805599453f : -INFINITY;
+  }
 }
+
+// ----------------------------------------------------------------- host
+// The pool as [pages * heads, page_size, D]: a box is one head's share of a
+// page, or 128 rows of it, 64 bf16 columns (one swizzle atom) or a whole
+// E4M3 row wide.  E4M3 tiles of 128-byte rows are swizzled as well, for the
+// conversion's reads.
+bool encode_pages(CUtensorMap* m, const void* base, const PagedBatch& p, bool f8) {
+  const int64_t es = f8 ? 1 : 2, ps = (int64_t)1 << p.page_shift;
+  const int64_t dims[3] = {p.head_dim, ps, (int64_t)p.num_pages * p.heads_kv};
+  const int64_t strides[2] = {p.head_dim * es, ps * p.head_dim * es};
+  const int box[3] = {f8 ? p.head_dim : 64, (int)std::min<int64_t>(ps, BN), 1};
+  return encode_3d(m, base, f8, dims, strides, box, !f8 || p.head_dim == 128);
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = 148;
+  }
+  return n;
+}
+
+// Query rows that one sequence can have at most; more than one tile of them
+// takes the two-tile kernel (each key tile then serves 256 rows).
+int64_t max_rows(const PagedAttnArgs& a) {
+  return (int64_t)std::min(a.p.max_new, a.p.total_new) * (a.heads_q / a.p.heads_kv);
+}
+
+template <int D, bool kF8, int kQT>
+cudaError_t launch_t(const PagedAttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, Params& p,
+                     int sms, cudaStream_t stream) {
+  using L = Lay<D, kF8, kQT>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(paged_attn_kernel<D, kF8, kQT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  });
+  if (attr != cudaSuccess) return attr;
+  cudaError_t e = launch_pdl(paged_attn_kernel<D, kF8, kQT>, dim3(sms), dim3(L::kThreads), L::kSmem,
+                             stream, mk, mv, p);
+  note_launch();
+  if (e != cudaSuccess) return e;
+  const int parts = (p.slot_rows + kMergeRows - 1) / kMergeRows;
+  e = launch_pdl(paged_merge_kernel<D, kQT>, dim3(sms * parts), dim3(kMergeWarps * 32), 0, stream, p);
+  note_launch();
+  return e;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t paged_attn_scratch_bytes(const PagedAttnArgs&) { return 0; }
+size_t paged_attn_scratch_bytes(const PagedAttnArgs& a) {
+  const size_t sms = num_sms();
+  const size_t rows = (size_t)std::min<int64_t>(max_rows(a), 2 * BM);
+  return align256(sms * sizeof(Split)) + align256(2 * sms * rows * sizeof(float2)) +
+         2 * sms * rows * a.p.head_dim * 2;
+}
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
-  if (a.p.head_dim == 64)
-    return a.pool.e4m3 ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
-  return a.pool.e4m3 ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);
+  const bool f8 = a.pool.e4m3;
+  const int D = a.p.head_dim;
+  const int64_t rows = max_rows(a);
+  if (rows == 0) return cudaSuccess;
+  CUtensorMap mk, mv;
+  if (!encode_pages(&mk, a.pool.k, a.p, f8) || !encode_pages(&mv, a.pool.v, a.p, f8))
+    return cudaErrorInvalidValue;
+  const int sms = num_sms();
+  Params p{};
+  p.b = a.p;
+  p.k_scale = a.pool.k_scale;
+  p.v_scale = a.pool.v_scale;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.q_stride = a.q_stride;
+  p.Hq = a.heads_q;
+  p.G = a.heads_q / a.p.heads_kv;
+  p.causal = a.causal ? 1 : 0;
+  p.max_ctas = sms;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.slot_rows = (int)std::min<int64_t>(rows, 2 * BM);
+  uint8_t* s = static_cast<uint8_t*>(a.scratch);
+  p.split = reinterpret_cast<Split*>(s);
+  s += align256(sms * sizeof(Split));
+  p.part_lse = reinterpret_cast<float2*>(s);
+  s += align256((size_t)2 * sms * p.slot_rows * sizeof(float2));
+  p.part_o = reinterpret_cast<uint32_t*>(s);
+  p.err = a.err;
+  p.wait_ns = pipeline_wait_ns();
+  p.stall = pipeline_test_stall() ? 1 : 0;
+  const bool two = rows > BM;
+#define DD_GO(d, f, q) return launch_t<d, f, q>(a, mk, mv, p, sms, stream)
+  if (D == 64) {
+    if (f8) {
+      if (two) DD_GO(64, true, 2);
+      DD_GO(64, true, 1);
+    }
+    if (two) DD_GO(64, false, 2);
+    DD_GO(64, false, 1);
+  }
+  if (f8) {
+    if (two) DD_GO(128, true, 2);
+    DD_GO(128, true, 1);
+  }
+  if (two) DD_GO(128, false, 2);
+  DD_GO(128, false, 1);
+#undef DD_GO
 }
 
 }  // namespace dd
