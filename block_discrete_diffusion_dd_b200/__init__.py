@@ -677,41 +677,56 @@ def _need(ok: bool, what: str):
 
 
 class _on:
-    """Makes `device` the current one around a call on its tensors."""
-    __slots__ = ("_guard",)
+    """Makes `device` the current one around a call on its tensors; as a value
+    of `with`, the stream to launch on: `stream`, or the device's current one
+    (its raw handle: a torch.cuda.Stream object costs more than a launch)."""
+    __slots__ = ("_guard", "_stream")
 
-    def __init__(self, device):
-        self._guard = (None if device.index is None or device.index == torch.cuda.current_device()
+    def __init__(self, device, stream):
+        self._guard = (None if device.index == torch._C._cuda_getDevice()
                        else torch.cuda.device(device))
+        self._stream = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+                        else stream.cuda_stream)
 
     def __enter__(self):
         if self._guard is not None:
             self._guard.__enter__()
+        return self._stream
 
     def __exit__(self, *exc):
         if self._guard is not None:
             self._guard.__exit__(*exc)
 
 
+def _lent(t: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor allocated here, on the current stream, for a call on `stream`:
+    its memory is not reused before that stream is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _packed(t: torch.Tensor, heads: int, dim: int, dtype, device, what: str) -> int:
     """Checks a packed [rows, heads, dim] tensor whose rows may lie apart (a
     view of a fused projection) and returns the elements between rows."""
-    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim,
-          f"{what}: shape {tuple(t.shape)}, expected [rows, {heads}, {dim}]")
-    _need(t.dtype == dtype and t.device == device,
-          f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected [rows, {heads}, {dim}]")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
     s = t.stride()
-    _need((dim == 1 or s[2] == 1) and (heads == 1 or s[1] == dim),
-          f"{what}: a row's [heads, dim] must be contiguous")
-    return s[0] if t.shape[0] > 1 else heads * dim
+    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+        raise ValueError(f"{what}: a row's [heads, dim] must be contiguous")
+    return s[0] if shape[0] > 1 else heads * dim
 
 
 def _dense(t: torch.Tensor, shape, dtype, device, what: str):
-    _need(tuple(t.shape) == tuple(shape),
-          f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _need(t.dtype == dtype and t.device == device,
-          f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
-    _need(t.is_contiguous(), f"{what} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
 
 
 class PagedCache:
@@ -773,11 +788,13 @@ class PagedBatch:
         _dense(kv_len, (B,), torch.int32, self.device, "kv_len")
         self.page_table, self.cu_new, self.kv_len, self.max_new = page_table, cu_new, kv_len, max_new
         self.batch = B
-        self._args = (B, pages)
-        self._ptrs = (page_table.data_ptr(), cu_new.data_ptr(), kv_len.data_ptr())
+        self._struct = _PagedBatchC(B, pages, 0, 0, page_table.data_ptr(), cu_new.data_ptr(),
+                                    kv_len.data_ptr())
 
     def _c(self, total_new: int):
-        return _PagedBatchC(*self._args, total_new, int(self.max_new), *self._ptrs)
+        c = self._struct
+        c.total_new, c.max_new = total_new, self.max_new
+        return c
 
 
 def cache_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -785,16 +802,16 @@ def cache_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     """dd_cache_append: writes bf16 k_new, v_new [total_new, heads_kv,
     head_dim] (rows may lie apart) at the batch's last positions."""
     lib, dev = load(), cache.device
-    _need(batch.device == dev, f"batch on {batch.device}, cache on {dev}")
+    _need(batch.device == dev, "the batch and the cache are on different devices")
     ks = _packed(k_new, cache.heads_kv, cache.head_dim, torch.bfloat16, dev, "k_new")
     vs = _packed(v_new, cache.heads_kv, cache.head_dim, torch.bfloat16, dev, "v_new")
     _need(k_new.shape[0] == v_new.shape[0], "k_new and v_new have different numbers of rows")
-    with _on(dev):
+    with _on(dev, stream) as st:
         if workspace is None:
-            workspace = new_workspace(int(lib.dd_cache_workspace()), dev, stream)
+            workspace = _lent(new_workspace(int(lib.dd_cache_workspace()), dev, stream), stream)
         _check(lib.dd_cache_append(cache._ref, batch._c(k_new.shape[0]), k_new.data_ptr(), ks,
                                    v_new.data_ptr(), vs, workspace.data_ptr(), workspace.numel(),
-                                   _stream(stream)))
+                                   st))
 
 
 def cache_read(cache: PagedCache, page_table: torch.Tensor, cu_prefix: torch.Tensor,
@@ -812,17 +829,17 @@ def cache_read(cache: PagedCache, page_table: torch.Tensor, cu_prefix: torch.Ten
     _need(total >= 0, f"total={total}")
     shape = (total, cache.heads_kv, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = _lent(torch.empty(shape, dtype=torch.bfloat16, device=dev), stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = _lent(torch.empty(shape, dtype=torch.bfloat16, device=dev), stream)
     _dense(k_out, shape, torch.bfloat16, dev, "k_out")
     _dense(v_out, shape, torch.bfloat16, dev, "v_out")
-    with _on(dev):
+    with _on(dev, stream) as st:
         if workspace is None:
-            workspace = new_workspace(int(lib.dd_cache_workspace()), dev, stream)
+            workspace = _lent(new_workspace(int(lib.dd_cache_workspace()), dev, stream), stream)
         _check(lib.dd_cache_read(cache._ref, B, pages, page_table.data_ptr(),
                                  cu_prefix.data_ptr(), total, k_out.data_ptr(), v_out.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                 workspace.data_ptr(), workspace.numel(), st))
     return k_out, v_out
 
 
@@ -842,21 +859,22 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, batch: PagedBatch,
     _need(q.dim() == 3, "q must be [total_new, heads_q, head_dim]")
     T, Hq = q.shape[0], q.shape[1]
     qs = _packed(q, Hq, D, torch.bfloat16, dev, "q")
-    _need(batch.device == dev, f"batch on {batch.device}, cache on {dev}")
+    _need(batch.device == dev, "the batch and the cache are on different devices")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = _lent(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev), stream)
     _dense(out, (T, Hq, D), torch.bfloat16, dev, "out")
     if want_lse and lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _lent(torch.empty((T, Hq), dtype=torch.float32, device=dev), stream)
     if lse is not None:
         _dense(lse, (T, Hq), torch.float32, dev, "lse")
-    with _on(dev):
+    with _on(dev, stream) as st:
         if workspace is None:
-            workspace = new_workspace(paged_attn_workspace_bytes(cache, batch, T, Hq), dev, stream)
+            workspace = _lent(new_workspace(paged_attn_workspace_bytes(cache, batch, T, Hq), dev,
+                                            stream), stream)
         _check(lib.dd_paged_attn(cache._ref, batch._c(T), Hq, q.data_ptr(), qs,
                                  float(scale if scale is not None else D ** -0.5), int(causal),
                                  out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                 workspace.data_ptr(), workspace.numel(), st))
     return out, lse
 
 
@@ -886,33 +904,39 @@ def verify_draft(target_logits: torch.Tensor, draft_logits: torch.Tensor,
     _need(target_logits.dim() == 2 and draft_logits.dim() == 2, "logits must be 2-D")
     T, V = draft_logits.shape
     B = u_sample.numel()
-    _need(tuple(target_logits.shape) == (T + B, V),
-          f"target_logits: shape {tuple(target_logits.shape)}, expected {(T + B, V)}")
-    for t, what in ((target_logits, "target_logits"), (draft_logits, "draft_logits")):
-        _need(t.dtype == target_logits.dtype and t.device == dev,
-              f"{what}: {t.dtype} on {t.device}, expected {target_logits.dtype} on {dev}")
-        _need(V == 1 or t.stride(1) == 1, f"{what}: a row must be contiguous")
+    if target_logits.shape != (T + B, V):
+        raise ValueError(f"target_logits: shape {tuple(target_logits.shape)}, "
+                         f"expected {(T + B, V)}")
+    zt, zd = target_logits.stride(), draft_logits.stride()
+    if draft_logits.dtype != target_logits.dtype or draft_logits.device != dev:
+        raise ValueError(f"draft_logits: {draft_logits.dtype} on {draft_logits.device}, "
+                         f"expected {target_logits.dtype} on {dev}")
+    if V > 1 and (zt[1] != 1 or zd[1] != 1):
+        raise ValueError("a row of logits must be contiguous")
     for t, n, dt, what in ((draft_tokens, T, torch.int32, "draft_tokens"),
                            (draft_conf, T, torch.float32, "draft_conf"),
                            (cu_draft, B + 1, torch.int32, "cu_draft"),
                            (u_accept, T, torch.float32, "u_accept"),
                            (u_sample, B, torch.float32, "u_sample")):
         _dense(t, (n,), dt, dev, what)
-    o = outputs if outputs is not None else verify_draft_outputs(B, T, dev)
+    o = outputs
+    if o is None:
+        o = {k: _lent(t, stream) for k, t in verify_draft_outputs(B, T, dev).items()}
     for name, n, dt in (("accepted", B, torch.int32), ("tokens", T + B, torch.int32),
                         ("target_prob", T, torch.float32)):
         _dense(o[name], (n,), dt, dev, name)
-    with _on(dev):
+    with _on(dev, stream) as st:
         if workspace is None:
-            workspace = new_workspace(verify_draft_workspace_bytes(B, T, V), dev, stream)
+            workspace = _lent(new_workspace(verify_draft_workspace_bytes(B, T, V), dev, stream),
+                              stream)
         prm = VerifyParams(float(temperature), float(draft_temperature))
         _check(lib.dd_verify_draft(
             ctypes.byref(prm), _dtype_code(target_logits), B, T, V, target_logits.data_ptr(),
-            target_logits.stride(0) if T + B > 1 else V, draft_logits.data_ptr(),
-            draft_logits.stride(0) if T > 1 else V, draft_tokens.data_ptr(),
+            zt[0] if T + B > 1 else V, draft_logits.data_ptr(),
+            zd[0] if T > 1 else V, draft_tokens.data_ptr(),
             draft_conf.data_ptr(), cu_draft.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
             o["accepted"].data_ptr(), o["tokens"].data_ptr(), o["target_prob"].data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream(stream)))
+            workspace.data_ptr(), workspace.numel(), st))
     return o
 
 

@@ -50,14 +50,16 @@
 // drains its copies and MMAs and frees its tensor memory.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
-#include "dd_paged.cuh"
+#include "dd_paged_attn.cuh"
 
 namespace dd {
 namespace {
 
+using namespace paged;
+
 constexpr int BM = 128;  // query rows per tile
-constexpr int BN = 128;  // keys per tile
 constexpr uint32_t kAtom = 128 * 128;  // 128 rows of one 128-byte swizzle atom (64 bf16)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 2 * BN;    // S buffers first
@@ -97,198 +99,6 @@ struct Lay {
   static_assert(kStages <= kMaxStages && kRawStages <= kMaxRaw, "barrier arrays");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
-
-// A partial item that starts in CTA c and ends in CTA `last`: its partials
-// are slot 1 of CTA c and slot 0 of CTAs c + 1 .. last.
-struct Split {
-  int b, g, tp, last;  // b < 0: none starts here
-};
-
-struct Params {
-  PagedBatch b;
-  const uint8_t *k_scale, *v_scale;
-  const __nv_bfloat16* q;
-  int64_t q_stride;
-  int Hq, G, causal, max_ctas;
-  float scale_log2;
-  __nv_bfloat16* out;
-  float* lse;
-  Split* split;       // [max_ctas]
-  int slot_rows;      // rows kept per slot
-  uint32_t* part_o;   // [2 max_ctas][slot_rows][D / 2]: O / l as fp16 pairs times 2^-e_row
-  float2* part_lse;   // [2 max_ctas][slot_rows]: log2-domain LSE, 2^e_row
-  uint32_t* err;
-  uint64_t wait_ns;
-  int stall;
-};
-
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
-
-__device__ __forceinline__ int row_exponent(float m) {
-  if (!(m > 0.f) || !(m <= 3.4e38f)) return 0;
-  return min(113, max(-126, ilogbf(m) - 14));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Query-tile groups of a sequence, and the key tiles of group tp.
-template <int kQT>
-__device__ __forceinline__ int tile_groups(const ChunkRow& r, int G) {
-  return cdiv(r.n * G, kQT * BM);
-}
-template <int kQT>
-__device__ __forceinline__ int key_tiles(const ChunkRow& r, int G, int causal, int tp) {
-  const int last = (min((tp + 1) * kQT * BM, r.n * G) - 1) / G;  // last token of the group
-  const int seen = causal ? r.len - r.n + last + 1 : r.len;
-  return cdiv(max(seen, 0), BN);
-}
-
-// One CTA's part of an item.
-struct Seg {
-  int b, g, tp;
-  ChunkRow r;
-  int t0, t1, nt;  // key tiles [t0, t1) of nt
-};
-
-// Walks a CTA's share [pos, end) of the items laid end to end.
-template <int kQT, int kFixed>
-struct Walk {
-  int64_t pos, end;
-  int b, g, tp, x;  // the item, and the place in it
-  ChunkRow r;
-  int groups;
-
-  __device__ __forceinline__ void load(const Params& p) {
-    r = chunk_row(p.b, b, p.err);
-    groups = tile_groups<kQT>(r, p.G);
-  }
-  __device__ __forceinline__ bool next(const Params& p, Seg& s) {
-    while (pos < end) {
-      while (groups == 0) {  // a sequence without new tokens
-        ++b;
-        load(p);
-      }
-      const int nt = key_tiles<kQT>(r, p.G, p.causal, tp);
-      const int w = nt + kFixed;
-      const int x1 = (int)min((int64_t)w, x + (end - pos));
-      s.b = b;
-      s.g = g;
-      s.tp = tp;
-      s.r = r;
-      s.nt = nt;
-      s.t0 = max(0, x - kFixed);
-      s.t1 = max(0, x1 - kFixed);
-      const bool some = s.t1 > s.t0 || (nt == 0 && x == 0);
-      pos += x1 - x;
-      x = x1;
-      if (x == w) {
-        x = 0;
-        if (++tp == groups) {
-          tp = 0;
-          if (++g == p.b.heads_kv) {
-            g = 0;
-            ++b;
-            if (pos < end) load(p);
-          }
-        }
-      }
-      if (some) return true;
-    }
-    return false;
-  }
-};
-
-// The share of this CTA: a block-wide prefix sum over the sequences.
-struct Share {
-  int64_t pos, end, total;
-  int ctas, b, g, tp, x;
-};
-
-template <int D, bool kF8, int kQT>
-__device__ int64_t seq_weight(const Params& p, int b) {
-  using L = Lay<D, kF8, kQT>;
-  const ChunkRow r = chunk_row(p.b, b, p.err);
-  const int groups = tile_groups<kQT>(r, p.G);
-  int64_t w = 0;
-  for (int tp = 0; tp < groups; ++tp) w += key_tiles<kQT>(r, p.G, p.causal, tp) + L::kFixed;
-  return w * p.b.heads_kv;
-}
-
-template <int D, bool kF8, int kQT>
-__device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
-  using L = Lay<D, kF8, kQT>;
-  constexpr int kT = L::kThreads, kW = kT / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // exclusive prefix of v over the block; *all gets the block's sum
-  auto scan = [&](int64_t v, int64_t* all) {
-    int64_t inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 31) warp_sums[warp] = inc;
-    __syncthreads();
-    int64_t before = 0, sum = 0;
-    for (int i = 0; i < kW; ++i) {
-      if (i < warp) before += warp_sums[i];
-      sum += warp_sums[i];
-    }
-    __syncthreads();
-    *all = sum;
-    return before + inc - v;
-  };
-  int64_t total = 0, w = 0, at = 0, all;
-  for (int b0 = 0; b0 < p.b.batch; b0 += kT) {
-    const int b = b0 + threadIdx.x;
-    w = b < p.b.batch ? seq_weight<D, kF8, kQT>(p, b) : 0;
-    at = scan(w, &all);
-    total += all;
-  }
-  // no CTA takes less than one item's overhead and as many tiles again
-  const int64_t most = (total + 2 * L::kFixed - 1) / (2 * L::kFixed);
-  const int ctas = (int)min((int64_t)gridDim.x, most);
-  const int64_t pos = ctas > 0 && blockIdx.x < ctas ? blockIdx.x * total / ctas : 0;
-  const int64_t end = ctas > 0 && blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : 0;
-  if (threadIdx.x == 0) {
-    sh->total = total;
-    sh->ctas = ctas;
-    sh->pos = pos;
-    sh->end = end;
-  }
-  if (end > pos) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < p.b.batch; b0 += kT) {
-      const int b = b0 + threadIdx.x;
-      if (p.b.batch > kT) {  // (a single round keeps its w and prefix)
-        w = b < p.b.batch ? seq_weight<D, kF8, kQT>(p, b) : 0;
-        at = scan(w, &all);
-      }
-      if (pos >= base + at && pos < base + at + w) {
-        int64_t off = pos - base - at;
-        const ChunkRow r = chunk_row(p.b, b, p.err);
-        const int64_t head = w / p.b.heads_kv;
-        sh->b = b;
-        sh->g = (int)(off / head);
-        off %= head;
-        int tp = 0;
-        while (true) {
-          const int wi = key_tiles<kQT>(r, p.G, p.causal, tp) + L::kFixed;
-          if (off < wi) break;
-          off -= wi;
-          ++tp;
-        }
-        sh->tp = tp;
-        sh->x = (int)off;
-      }
-      base += all;
-    }
-  }
-  __syncthreads();
-}
 
 __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t off) {
   return base + (uint64_t)(off >> 4);
@@ -369,21 +179,14 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  find_share<D, kF8, kQT>(p, &share, warp_sums);
+  find_share<kQT * BM, L::kFixed, L::kThreads>(p, &share, warp_sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  Walk<kQT, L::kFixed> walk;
-  walk.pos = share.pos;
-  walk.end = share.end;
+  auto walk = start_walk<kQT * BM, L::kFixed>(p, share);
   const bool work = walk.pos < walk.end;
-  walk.b = share.b;
-  walk.g = share.g;
-  walk.tp = share.tp;
-  walk.x = share.x;
-  if (work) walk.load(p);
   Seg sg;
 
   if (warp == L::kWarpTMA) {
@@ -889,31 +692,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
     }
   }
 
-  if (threadIdx.x == 0) {
-    // the item that starts in this CTA's share and ends in a later one
-    Split s{-1, 0, 0, 0};
-    Walk<kQT, L::kFixed> w;
-    w.pos = share.pos;
-    w.end = share.end;
-    if (blockIdx.x < share.ctas && w.pos < w.end) {
-      w.b = share.b;
-      w.g = share.g;
-      w.tp = share.tp;
-      w.x = share.x;
-      w.load(p);
-      Seg e;
-      while (w.next(p, e))
-        if (e.t0 == 0 && e.t1 < e.nt && e.t1 > 0) {
-          // its last unit, and the CTA whose share holds it
-          const int64_t last = share.end + (e.nt - e.t1) - 1;
-          int c = (int)(last * share.ctas / share.total);
-          while ((c + 1) * share.total / share.ctas <= last) ++c;
-          while (c * share.total / share.ctas > last) --c;
-          s = Split{e.b, e.g, e.tp, c};
-        }
-    }
-    p.split[blockIdx.x] = s;
-  }
+  if (threadIdx.x == 0) write_split<kQT * BM, L::kFixed>(p, share);
   if (*abort_flag && threadIdx.x == 0) atomicOr(p.err, kDevErrTimeout);
   tc_fence_before();
   __syncthreads();
@@ -927,7 +706,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
 // lane l the columns (D / 32) l ..
 constexpr int kMergeWarps = 8, kMergeRows = 16;
 
-template <int D, int kQT>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Params p) {
   constexpr int kC = D / 64;  // fp16 pairs per lane
   pdl_wait();
@@ -937,7 +716,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Par
   const Split s = p.split[c];
   if (s.b < 0) return;
   const ChunkRow r = chunk_row(p.b, s.b, p.err);
-  const int row0 = s.tp * kQT * BM, rows = min(r.n * p.G - row0, p.slot_rows);
+  const int row0 = s.tp * kRows, rows = min(r.n * p.G - row0, p.slot_rows);
   const int ns = s.last - c + 1;
   if (ns < 1 || s.last >= p.max_ctas) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1032,8 +811,8 @@ int64_t max_rows(const PagedAttnArgs& a) {
 }
 
 template <int D, bool kF8, int kQT>
-cudaError_t launch_t(const PagedAttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, Params& p,
-                     int sms, cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, int sms,
+                     cudaStream_t stream) {
   using L = Lay<D, kF8, kQT>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
@@ -1045,32 +824,40 @@ cudaError_t launch_t(const PagedAttnArgs& a, const CUtensorMap& mk, const CUtens
   cudaError_t e = launch_pdl(paged_attn_kernel<D, kF8, kQT>, dim3(sms), dim3(L::kThreads), L::kSmem,
                              stream, mk, mv, p);
   note_launch();
-  if (e != cudaSuccess) return e;
+  return e;
+}
+
+template <int D, int kRows>
+cudaError_t launch_merge(const Params& p, cudaStream_t stream) {
   const int parts = (p.slot_rows + kMergeRows - 1) / kMergeRows;
-  e = launch_pdl(paged_merge_kernel<D, kQT>, dim3(sms * parts), dim3(kMergeWarps * 32), 0, stream, p);
+  cudaError_t e = launch_pdl(paged_merge_kernel<D, kRows>, dim3(p.max_ctas * parts),
+                             dim3(kMergeWarps * 32), 0, stream, p);
   note_launch();
   return e;
 }
+
+// CTAs whose partials a call keeps.
+int max_ctas(int64_t rows) { return (rows <= kFewRows ? 2 : 1) * num_sms(); }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
 size_t paged_attn_scratch_bytes(const PagedAttnArgs& a) {
-  const size_t sms = num_sms();
-  const size_t rows = (size_t)std::min<int64_t>(max_rows(a), 2 * BM);
-  return align256(sms * sizeof(Split)) + align256(2 * sms * rows * sizeof(float2)) +
-         2 * sms * rows * a.p.head_dim * 2;
+  const int64_t most = max_rows(a);
+  const size_t ctas = max_ctas(most), rows = (size_t)std::min<int64_t>(most, 2 * BM);
+  return align256(ctas * sizeof(Split)) + align256(2 * ctas * rows * sizeof(float2)) +
+         2 * ctas * rows * a.p.head_dim * 2;
 }
 
+// Up to kFewRows query rows per sequence and kv head, the kernel for few rows
+// (dd_paged_few.cu); up to one tile of them the tensor-core kernel with one
+// query tile; above that with two, so that a key tile serves 256 rows.
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   const bool f8 = a.pool.e4m3;
   const int D = a.p.head_dim;
   const int64_t rows = max_rows(a);
   if (rows == 0) return cudaSuccess;
-  CUtensorMap mk, mv;
-  if (!encode_pages(&mk, a.pool.k, a.p, f8) || !encode_pages(&mv, a.pool.v, a.p, f8))
-    return cudaErrorInvalidValue;
   const int sms = num_sms();
   Params p{};
   p.b = a.p;
@@ -1081,37 +868,42 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   p.Hq = a.heads_q;
   p.G = a.heads_q / a.p.heads_kv;
   p.causal = a.causal ? 1 : 0;
-  p.max_ctas = sms;
+  p.max_ctas = max_ctas(rows);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   p.slot_rows = (int)std::min<int64_t>(rows, 2 * BM);
   uint8_t* s = static_cast<uint8_t*>(a.scratch);
   p.split = reinterpret_cast<Split*>(s);
-  s += align256(sms * sizeof(Split));
+  s += align256(p.max_ctas * sizeof(Split));
   p.part_lse = reinterpret_cast<float2*>(s);
-  s += align256((size_t)2 * sms * p.slot_rows * sizeof(float2));
+  s += align256((size_t)2 * p.max_ctas * p.slot_rows * sizeof(float2));
   p.part_o = reinterpret_cast<uint32_t*>(s);
   p.err = a.err;
   p.wait_ns = pipeline_wait_ns();
   p.stall = pipeline_test_stall() ? 1 : 0;
+  if (rows <= kFewRows) {
+    const cudaError_t e = launch_few(p, a.pool, (int)rows, sms, stream);
+    if (e != cudaSuccess) return e;
+    return D == 64 ? launch_merge<64, kFewRows>(p, stream) : launch_merge<128, kFewRows>(p, stream);
+  }
+  CUtensorMap mk, mv;
+  if (!encode_pages(&mk, a.pool.k, a.p, f8) || !encode_pages(&mv, a.pool.v, a.p, f8))
+    return cudaErrorInvalidValue;
   const bool two = rows > BM;
-#define DD_GO(d, f, q) return launch_t<d, f, q>(a, mk, mv, p, sms, stream)
-  if (D == 64) {
-    if (f8) {
-      if (two) DD_GO(64, true, 2);
-      DD_GO(64, true, 1);
-    }
-    if (two) DD_GO(64, false, 2);
-    DD_GO(64, false, 1);
-  }
-  if (f8) {
-    if (two) DD_GO(128, true, 2);
-    DD_GO(128, true, 1);
-  }
-  if (two) DD_GO(128, false, 2);
-  DD_GO(128, false, 1);
-#undef DD_GO
+  auto go = [&](auto d, auto e4m3) {
+    constexpr int kD = decltype(d)::value;
+    constexpr bool k8 = decltype(e4m3)::value;
+    cudaError_t e = two ? launch_t<kD, k8, 2>(mk, mv, p, sms, stream)
+                        : launch_t<kD, k8, 1>(mk, mv, p, sms, stream);
+    if (e != cudaSuccess) return e;
+    return two ? launch_merge<kD, 2 * BM>(p, stream) : launch_merge<kD, BM>(p, stream);
+  };
+  using std::integral_constant;
+  using D64 = integral_constant<int, 64>;
+  using D128 = integral_constant<int, 128>;
+  if (D == 64) return f8 ? go(D64{}, std::true_type{}) : go(D64{}, std::false_type{});
+  return f8 ? go(D128{}, std::true_type{}) : go(D128{}, std::false_type{});
 }
 
 }  // namespace dd

@@ -1,0 +1,452 @@
+// dd_paged_few.cu -- attention over a paged cache for few query rows: one
+// token per sequence, or a few (dd_paged_attn with at most kFewRows packed
+// rows per sequence and kv head).
+//
+// What bounds it is the cache: every key and value is read once and serves
+// only a handful of rows, so the products are a small part of the time and
+// what counts is bytes in flight (about 45 KB per SM cover the latency at the
+// full rate).  A 128-row tensor-core tile would leave one warp with all the
+// softmax; here each warp works on its own 16 keys at a time with warp-level
+// matrix instructions (m16n8k16, keys as the 16 rows, query rows as the 8
+// columns) and its own running softmax, with no barrier in the loop, and the
+// warps' results are merged at the end of an item.
+//
+// No operand passes through shared memory: the order in which the head
+// dimension is summed, and the order of output columns, are free, so each lane
+// loads 16 consecutive bytes of a row of K or V and uses them as the fragment
+// of permuted columns:
+//   S^T = K Q^T   lane (g, c) = (lane / 4, lane % 4) holds, of keys g and
+//                 g + 8, the 16 bytes at 64 j + 16 c for each 64-byte block j;
+//                 Q is loaded in the same order;
+//   O^T += V^T W  lane (g, c) holds, of keys 2c, 2c+1, 2c+8, 2c+9, the D / 8
+//                 columns from g D / 8 on; byte permutes pair two keys of one
+//                 column, the columns 2t and 2t + 1 of the lane being rows g
+//                 and g + 8 of the t-th product;
+//   W             the softmax weights come out of the first product by key
+//                 and enter the second by query row: one 8x8 transpose each.
+//
+// E4M3 cache: a code is exact in fp16, and the products run on the codes
+// themselves, in fp16.  The key's scale 2^ek multiplies its scores.  The
+// value's scale 2^ev enters the exponent: with x the log2-domain score, the
+// weights are w = 2^(x + ev - m) with m the running maximum of x + ev, so
+// that O = sum w code is always within fp16's range, and the softmax's sum is
+// that of 2^(x - m) = w 2^-ev.  The bf16 query is scaled by a power of two per
+// row that puts its largest magnitude in [2^14, 2^15); only what lies 2^28
+// below it loses bits.
+#include <mutex>
+
+#include "dd_paged_attn.cuh"
+
+namespace dd {
+namespace paged {
+namespace {
+
+constexpr int kFixed = 2;  // an item's overhead in key tiles
+constexpr float kLazy = 8.0f;
+
+// Warps per CTA and CTAs per SM by what a lane has to keep: 16 keys of data
+// (32 registers for 8-bit, 64 for bf16, at D = 128), the output (D / 4 per 8
+// query rows) and the query.
+template <int D, bool kF8, int NT>
+struct Few {
+  static constexpr bool kSmall = kF8 ? NT == 1 : NT == 1 && D == 64;
+  static constexpr int kWarps = kSmall ? 8 : NT == 1 ? 10 : 8;
+  static constexpr int kBlocks = kSmall ? 2 : 1;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kLd = D + 4;  // floats per row of the merge area
+  static constexpr int kSmem = kWarps * kRows * (kLd + 2) * 4;
+};
+
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p));
+  return v;
+}
+
+// C (16 x 8, fp32) += A (16 x 16) B (16 x 8).
+template <bool kF16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two E4M3 codes (the low or high half of w) as fp16, exact.
+__device__ __forceinline__ uint32_t f16_of(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+template <int D, bool kF8, int NT>
+__global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kBlocks)
+    paged_few_kernel(const Params p, const uint8_t* __restrict__ k_pool,
+                     const uint8_t* __restrict__ v_pool) {
+  using F = Few<D, kF8, NT>;
+  constexpr int kRow = kF8 ? D : 2 * D;   // bytes of a token's row
+  constexpr int kJ = kRow / 64;           // 64-byte blocks of it
+  constexpr int kKS = kF8 ? 4 : 2;        // products per block
+  constexpr int kMT = D / 16;             // products per 16 keys of V
+  constexpr int kVB = kRow / 8;           // bytes of a V row per lane
+  extern __shared__ float area[];         // merge area: O, then m and l
+  __shared__ Share share;
+  __shared__ int64_t warp_sums[F::kWarps];
+  float* area_m = area + F::kWarps * F::kRows * F::kLd;
+  float* area_l = area_m + F::kWarps * F::kRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  find_share<F::kRows, kFixed, F::kThreads>(p, &share, warp_sums);
+  auto walk = start_walk<F::kRows, kFixed>(p, share);
+  const int shift = p.b.page_shift, in_page = (1 << shift) - 1;
+  Seg sg;
+  while (walk.next(p, sg)) {
+    const int rows = sg.r.n * p.G;
+    const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
+    // ---- the query rows nt 8 + g as fragments, and what rows 2c, 2c + 1 need
+    uint32_t qf[NT][kJ * kKS * 2];
+    float scale[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      const int tok = r / p.G;
+      const __nv_bfloat16* src = p.q + (int64_t)(sg.r.q0 + min(tok, max(sg.r.n - 1, 0))) * p.q_stride +
+                                 (int64_t)(sg.g * p.G + r - tok * p.G) * D;
+      float mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        // 16 (8-bit cache) or 8 (bf16 cache) consecutive elements
+        constexpr int kE = kF8 ? 2 : 1;
+#pragma unroll
+        for (int h = 0; h < kE; ++h) {
+          const uint4 v = r < rows ? ld16(src + j * (kF8 ? 64 : 32) + c * (kF8 ? 16 : 8) + h * 8)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t* f = &qf[nt][(j * kE + h) * 4];
+          f[0] = v.x;
+          f[1] = v.y;
+          f[2] = v.z;
+          f[3] = v.w;
+        }
+      }
+      float mul = p.scale_log2;
+      if constexpr (kF8) {
+#pragma unroll
+        for (int i = 0; i < kJ * kKS * 2; ++i)
+          mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qf[nt][i])), fabsf(bf16hi(qf[nt][i]))));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = row_exponent(mx);
+        const float inv = pow2f(-e);
+#pragma unroll
+        for (int i = 0; i < kJ * kKS * 2; ++i)
+          qf[nt][i] = pack_f16x2(bf16lo(qf[nt][i]) * inv, bf16hi(qf[nt][i]) * inv);
+        mul *= pow2f(e);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        scale[nt][u] = __shfl_sync(0xffffffffu, mul, (2 * c + u) * 4);
+        const int row = nt * 8 + 2 * c + u;
+        lim[nt][u] = row >= rows ? 0 : p.causal ? sg.r.len - sg.r.n + row / p.G + 1 : sg.r.len;
+      }
+    }
+    // ---- the keys of this warp: chunks of 16, every kWarps-th of the segment
+    float o[NT][kMT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -1e30f;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < kMT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.f;
+    }
+    const int32_t* table = p.b.page_table + (int64_t)sg.b * p.b.max_pages;
+    const int first = sg.t0 * (BN / 16) + warp;
+    const int last = min(sg.t1 * (BN / 16), cdiv(sg.r.len, 16));  // chunks end
+    // pool row of position 16 i + 8 h (its 8 keys share a page), or -1
+    auto look = [&](int i, int h) -> int64_t {
+      const int pos = i * 16 + h * 8;
+      if (i >= last || pos >= sg.r.len) return -1;
+      const int page = __ldg(table + (pos >> shift));
+      if ((uint32_t)page >= (uint32_t)p.b.num_pages) {
+        atomicOr(p.err, kDevErrBounds);
+        return -1;
+      }
+      return (((int64_t)page * p.b.heads_kv + sg.g) << shift) + (pos & in_page);
+    };
+    uint4 kd[2][kJ];                              // keys g, g + 8
+    uint4 vd[4][(kVB + 15) / 16];                 // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};  // scale exponents of keys g, g + 8
+    auto load_k = [&](int i, const int64_t (&row)[2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = row[h] >= 0 && i * 16 + h * 8 + g < sg.r.len;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+          kd[h][j] = ok ? ld16(k_pool + (row[h] + g) * kRow + j * 64 + c * 16)
+                        : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kF8) {
+          ks[h] = ok ? (float)((int)__ldg(p.k_scale + row[h] + g) - 127) : 0.f;
+          vs[h] = ok ? (float)((int)__ldg(p.v_scale + row[h] + g) - 127) : 0.f;
+        }
+      }
+    };
+    auto load_v = [&](int i, const int64_t (&row)[2]) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int h = u >> 1, key = 2 * c + (u & 1);
+        const bool ok = row[h] >= 0 && i * 16 + h * 8 + key < sg.r.len;
+        const uint8_t* src = v_pool + (row[h] + key) * kRow + g * kVB;
+        if constexpr (kVB >= 16) {
+#pragma unroll
+          for (int e = 0; e < kVB / 16; ++e)
+            vd[u][e] = ok ? ld16(src + e * 16) : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          const uint2 x = ok ? ld8(src) : make_uint2(0u, 0u);
+          vd[u][0] = make_uint4(x.x, x.y, 0u, 0u);
+        }
+      }
+    };
+    int64_t row[2] = {look(first, 0), look(first, 1)};
+    load_k(first, row);
+    load_v(first, row);
+    for (int i = first; i < last; i += F::kWarps) {
+      const int64_t nrow[2] = {look(i + F::kWarps, 0), look(i + F::kWarps, 1)};
+      // ---- S^T: keys g, g + 8 by query rows 2c, 2c + 1
+      float s[NT][4] = {};
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const uint32_t a[4] = {kd[0][j].x, kd[0][j].y, kd[0][j].z, kd[0][j].w};
+        const uint32_t b[4] = {kd[1][j].x, kd[1][j].y, kd[1][j].z, kd[1][j].w};
+#pragma unroll
+        for (int x = 0; x < kKS; ++x) {
+          uint32_t a0, a1, a2, a3;
+          if constexpr (kF8) {
+            a0 = f16_of(a[x]);
+            a2 = f16_of(a[x] >> 16);
+            a1 = f16_of(b[x]);
+            a3 = f16_of(b[x] >> 16);
+          } else {
+            a0 = a[2 * x];
+            a2 = a[2 * x + 1];
+            a1 = b[2 * x];
+            a3 = b[2 * x + 1];
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t* f = &qf[nt][(j * kKS + x) * 2];
+            mma<kF8>(s[nt], a0, a1, a2, a3, f[0], f[1]);
+          }
+        }
+      }
+      const float ek[2] = {ks[0], ks[1]}, ev[2] = {vs[0], vs[1]};
+      load_k(i + F::kWarps, nrow);  // in flight over the rest of this chunk
+      // ---- softmax
+      float fk[2], fv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        fk[h] = kF8 ? pow2f((int)ek[h]) : 1.f;
+        fv[h] = kF8 ? pow2f(-(int)ev[h]) : 1.f;
+      }
+      uint32_t wf[NT][2];
+      bool grow = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = e >> 1, u = e & 1;
+          const float x = kF8 ? fmaf(s[nt][e], fk[h] * scale[nt][u], ev[h]) : s[nt][e] * scale[nt][u];
+          s[nt][e] = i * 16 + h * 8 + g < lim[nt][u] ? x : -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float v = fmaxf(s[nt][u], s[nt][2 + u]);
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          mx[nt][u] = v;
+          grow |= v > m[nt][u] + kLazy;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float mn = fmaxf(m[nt][u], mx[nt][u]);
+            const float al = ex2_approx(m[nt][u] - mn);
+            m[nt][u] = mn;
+            l[nt][u] *= al;
+#pragma unroll
+            for (int t = 0; t < kMT; ++t) {
+              o[nt][t][u] *= al;
+              o[nt][t][2 + u] *= al;
+            }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = ex2_approx(s[nt][e] - m[nt][e & 1]);
+          l[nt][e & 1] = kF8 ? fmaf(w[e], fv[e >> 1], l[nt][e & 1]) : l[nt][e & 1] + w[e];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          wf[nt][h] = transpose8(kF8 ? pack_f16x2(w[2 * h], w[2 * h + 1])
+                                     : pack_bf16x2(w[2 * h], w[2 * h + 1]));
+      }
+      // ---- O^T
+#pragma unroll
+      for (int t = 0; t < kMT; ++t) {
+        uint32_t h[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (kF8) {
+            const uint4& q = vd[u][0];
+            const uint32_t word = (t >> 1) == 0 ? q.x : (t >> 1) == 1 ? q.y : (t >> 1) == 2 ? q.z : q.w;
+            h[u] = f16_of((t & 1) ? word >> 16 : word);
+          } else {
+            const uint4& q = vd[u][t >> 2];
+            h[u] = (t & 3) == 0 ? q.x : (t & 3) == 1 ? q.y : (t & 3) == 2 ? q.z : q.w;
+          }
+        }
+        const uint32_t a0 = __byte_perm(h[0], h[1], 0x5410), a1 = __byte_perm(h[0], h[1], 0x7632);
+        const uint32_t a2 = __byte_perm(h[2], h[3], 0x5410), a3 = __byte_perm(h[2], h[3], 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma<kF8>(o[nt][t], a0, a1, a2, a3, wf[nt][0], wf[nt][1]);
+      }
+      load_v(i + F::kWarps, nrow);
+    }
+    // ---- this warp's rows into the merge area
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float v = l[nt][u];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        const int r = warp * F::kRows + nt * 8 + 2 * c + u;
+        if (g == 0) {
+          area_m[r] = m[nt][u];
+          area_l[r] = v;
+        }
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+          *reinterpret_cast<float2*>(area + r * F::kLd + g * (D / 8) + 2 * t) =
+              make_float2(o[nt][t][u], o[nt][t][2 + u]);
+      }
+    __syncthreads();
+    // ---- one warp per query row, D / 32 columns per lane
+    constexpr int kC = D / 32;
+    for (int r = warp; r < min(rows, F::kRows); r += F::kWarps) {
+      float top = -1e30f;
+#pragma unroll
+      for (int w = 0; w < F::kWarps; ++w) top = fmaxf(top, area_m[w * F::kRows + r]);
+      float sum = 0.f, acc[kC] = {};
+#pragma unroll
+      for (int w = 0; w < F::kWarps; ++w) {
+        const float f = ex2_approx(area_m[w * F::kRows + r] - top);
+        sum = fmaf(f, area_l[w * F::kRows + r], sum);
+        const float* src = area + (w * F::kRows + r) * F::kLd + lane * kC;
+#pragma unroll
+        for (int e = 0; e < kC; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float lse = sum > 0.f ? top + __log2f(sum) : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kC; ++e) acc[e] *= inv;
+      if (whole) {
+        const int tok = r / p.G;
+        const int64_t at = (int64_t)(sg.r.q0 + tok) * p.Hq + sg.g * p.G + r - tok * p.G;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D) + lane * (kC / 2);
+#pragma unroll
+        for (int e = 0; e < kC / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e], acc[2 * e + 1]);
+        if (p.lse && lane == 0) p.lse[at] = lse * 0.6931471805599453f;
+      } else {
+        float mxa = 0.f;
+#pragma unroll
+        for (int e = 0; e < kC; ++e) mxa = fmaxf(mxa, fabsf(acc[e]));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, s));
+        const int e2 = row_exponent(mxa);
+        const float f = pow2f(-e2);
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (sg.t0 > 0 ? 0 : 1)) * p.slot_rows + r;
+        uint32_t* dst = p.part_o + slot * (D / 2) + lane * (kC / 2);
+#pragma unroll
+        for (int e = 0; e < kC / 2; ++e) dst[e] = pack_f16x2(acc[2 * e] * f, acc[2 * e + 1] * f);
+        if (lane == 0) p.part_lse[slot] = make_float2(lse, pow2f(e2));
+      }
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) write_split<F::kRows, kFixed>(p, share);
+}
+
+template <int D, bool kF8, int NT>
+cudaError_t launch_t(Params& p, const PagedPool& pool, int sms, cudaStream_t stream) {
+  using F = Few<D, kF8, NT>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(paged_few_kernel<D, kF8, NT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+  });
+  if (attr != cudaSuccess) return attr;
+  p.max_ctas = F::kBlocks * sms;
+  cudaError_t e = launch_pdl(paged_few_kernel<D, kF8, NT>, dim3(p.max_ctas),
+                             dim3(F::kThreads), F::kSmem, stream, p,
+                             static_cast<const uint8_t*>(pool.k),
+                             static_cast<const uint8_t*>(pool.v));
+  note_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_few(Params& p, const PagedPool& pool, int rows, int sms,
+                       cudaStream_t stream) {
+  const bool two = rows > 8;
+  if (p.b.head_dim == 64) {
+    if (pool.e4m3)
+      return two ? launch_t<64, true, 2>(p, pool, sms, stream) : launch_t<64, true, 1>(p, pool, sms, stream);
+    return two ? launch_t<64, false, 2>(p, pool, sms, stream) : launch_t<64, false, 1>(p, pool, sms, stream);
+  }
+  if (pool.e4m3)
+    return two ? launch_t<128, true, 2>(p, pool, sms, stream) : launch_t<128, true, 1>(p, pool, sms, stream);
+  return two ? launch_t<128, false, 2>(p, pool, sms, stream) : launch_t<128, false, 1>(p, pool, sms, stream);
+}
+
+}  // namespace paged
+}  // namespace dd

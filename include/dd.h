@@ -517,8 +517,8 @@ DD_API dd_status dd_denoise_block_adaptive_graph_destroy(dd_adaptive_graph graph
  *   k, v        [num_pages, heads_kv, page_size, head_dim] of dtype
  *   k_scale, v_scale  uint8 [num_pages, heads_kv, page_size] for DD_E4M3:
  *               byte s scales its (position, head) by 2^(s - 127) (the E8M0
- *               encoding; the library writes 7..247, and reading takes
- *               1..254); ignored for DD_BF16 */
+ *               encoding; 7..247 is what the library writes and what it
+ *               reads); ignored for DD_BF16 */
 typedef struct {
   int num_pages, page_size, heads_kv, head_dim;
   dd_dtype dtype;
