@@ -1182,6 +1182,10 @@ dd_status check_heads_q(int heads_q, int heads_kv) {
 
 }  // namespace
 
+// Behind the header, the workspaces of this family keep the counters of the
+// attention's merge, so that its calls may share one with the others.
+static constexpr size_t kPagedHeader = kHeaderBytes + kPagedCounters * sizeof(uint32_t);
+
 size_t dd_cache_workspace(void) { return kHeaderBytes; }
 
 dd_status dd_cache_append(const dd_paged_cache* cache, const dd_paged_batch* batch,
@@ -1250,7 +1254,7 @@ size_t dd_paged_attn_workspace(const dd_paged_cache* cache, const dd_paged_batch
   a.p = paged_batch(cache, batch);
   a.pool = paged_pool(cache);
   a.heads_q = heads_q;
-  return kHeaderBytes + paged_attn_scratch_bytes(a);
+  return kPagedHeader + paged_attn_scratch_bytes(a);
 }
 
 dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch, int heads_q,
@@ -1276,7 +1280,7 @@ dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch
   a.pool = paged_pool(cache);
   a.heads_q = heads_q;
   if ((st = check_workspace(workspace, workspace_bytes,
-                            kHeaderBytes + paged_attn_scratch_bytes(a))) != DD_OK)
+                            kPagedHeader + paged_attn_scratch_bytes(a))) != DD_OK)
     return st;
   a.q = q;
   a.q_stride = q_stride;
@@ -1285,7 +1289,8 @@ dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch
   a.out = out;
   a.lse = lse;
   a.err = static_cast<uint32_t*>(workspace);
-  a.scratch = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+  a.arrived = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+  a.scratch = static_cast<uint8_t*>(workspace) + kPagedHeader;
   cudaError_t e = launch_paged_attn(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged attention");
   return DD_OK;
@@ -1293,7 +1298,7 @@ dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch
 
 size_t dd_verify_draft_workspace(int batch, int total, int vocab) {
   if (batch < 0 || total < 0 || vocab < 1) return 0;
-  return kHeaderBytes + verify_scratch_bytes(batch, total, vocab);
+  return kPagedHeader + verify_scratch_bytes(batch, total, vocab);
 }
 
 dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int batch, int total,
@@ -1326,7 +1331,7 @@ dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int ba
   if (!aligned16(target_logits) || (total > 0 && !aligned16(draft_logits)))
     return fail(DD_ERR_INVALID_ARG, "logits pointers must be 16-byte aligned");
   dd_status st = check_workspace(workspace, workspace_bytes,
-                                 kHeaderBytes + verify_scratch_bytes(batch, total, vocab));
+                                 kPagedHeader + verify_scratch_bytes(batch, total, vocab));
   if (st != DD_OK) return st;
   VerifyArgs a{};
   a.target = target_logits;
@@ -1348,7 +1353,7 @@ dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int ba
   a.tokens = tokens;
   a.target_prob = target_prob;
   a.err = static_cast<uint32_t*>(workspace);
-  a.scratch = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+  a.scratch = static_cast<uint8_t*>(workspace) + kPagedHeader;
   cudaError_t e = launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "draft verification");
   return DD_OK;

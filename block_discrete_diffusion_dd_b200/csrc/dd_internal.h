@@ -214,8 +214,10 @@ struct PagedAttnArgs {
   void* out;   // bf16 [total_new, heads_q, head_dim]
   float* lse;  // fp32 [total_new, heads_q] or NULL
   uint32_t* err;
-  void* scratch;  // paged_attn_scratch_bytes
+  uint32_t* arrived;  // kPagedCounters, zero before the first call and after every call
+  void* scratch;      // paged_attn_scratch_bytes
 };
+constexpr size_t kPagedCounters = 1024;  // at least twice the SMs
 size_t paged_attn_scratch_bytes(const PagedAttnArgs& a);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 

@@ -95,7 +95,8 @@ struct Lay {
   static constexpr uint32_t kOffBar = kOffScale + kRawStages * BN;
   static constexpr uint32_t kSmem = kOffBar + sizeof(Barriers) + 1024;
   // an item's overhead (its Q tile, first product and epilogue) in key tiles
-  static constexpr int kFixed = kQT == 1 ? 2 : 4;
+  static constexpr int kFixed = kQT == 1 ? 2 : 3;
+  static constexpr int kMinShare = kFixed;
   static_assert(kStages <= kMaxStages && kRawStages <= kMaxRaw, "barrier arrays");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  find_share<kQT * BM, L::kFixed, L::kThreads>(p, &share, warp_sums);
+  find_share<kQT * BM, L::kFixed, L::kMinShare, L::kThreads>(p, &share, warp_sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
 
   auto walk = start_walk<kQT * BM, L::kFixed>(p, share);
   const bool work = walk.pos < walk.end;
-  Seg sg;
+  Seg sg{};
 
   if (warp == L::kWarpTMA) {
     // ------------------------------------------------------------ TMA
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
         page = after;
       }
     }
+    if (lane == 0) write_split<L::kFixed>(p, share, sg);
     // copies still in flight must land before the CTA exits (all have, unless
     // the CTA gave up: then the last tiles' barriers are waited for, those of
     // copies that were not issued any more running out)
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       const int first_head = sg.g * p.G;
       // global row (token, head) of the tile's row r, in elements of q / out
       auto token = [&](int r, int& head) {
-        const int pr = row0 + r, i = pr / p.G;
+        const int pr = row0 + r, i = div_G(p, pr);
         head = first_head + pr - i * p.G;
         return sg.r.q0 + i;
       };
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       // keys seen by rows A and B, and the fewest of the warp's rows
       auto limit = [&](int r) {
         if (r >= rows) return 0;
-        const int i = (row0 + r) / p.G;
+        const int i = div_G(p, row0 + r);
         return p.causal ? sg.r.len - sg.r.n + i + 1 : sg.r.len;
       };
       const int limA = limit(rA), limB = limit(rB), lim0 = limit(rbase);
@@ -692,7 +694,6 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
     }
   }
 
-  if (threadIdx.x == 0) write_split<kQT * BM, L::kFixed>(p, share);
   if (*abort_flag && threadIdx.x == 0) atomicOr(p.err, kDevErrTimeout);
   tc_fence_before();
   __syncthreads();
@@ -700,85 +701,19 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
   if (warp == L::kWarpMMA) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges an item's partials: lse = log2 sum 2^lse_s, O = sum_s 2^(lse_s - lse)
-// 2^e_s O_s.  Block (c, part) takes kMergeRows rows of the item that starts in
-// CTA c; a warp takes one row at a time, lane s the weight of split s and
-// lane l the columns (D / 32) l ..
+// Block (c, part): kMergeRows rows of the item that starts in CTA c and ends
+// in another.
 constexpr int kMergeWarps = 8, kMergeRows = 16;
 
 template <int D, int kRows>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Params p) {
-  constexpr int kC = D / 64;  // fp16 pairs per lane
   pdl_wait();
   pdl_trigger();
   const int parts = cdiv(p.slot_rows, kMergeRows);
-  const int c = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int c = blockIdx.x / parts, begin = blockIdx.x % parts * kMergeRows;
   const Split s = p.split[c];
-  if (s.b < 0) return;
-  const ChunkRow r = chunk_row(p.b, s.b, p.err);
-  const int row0 = s.tp * kRows, rows = min(r.n * p.G - row0, p.slot_rows);
-  const int ns = s.last - c + 1;
-  if (ns < 1 || s.last >= p.max_ctas) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = warp; i < kMergeRows; i += kMergeWarps) {
-    const int row = part * kMergeRows + i;
-    if (row >= rows) break;
-    auto at = [&](int k) {  // row of split k
-      return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.slot_rows + row;
-    };
-    float mx = -INFINITY;
-    for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, __ldcg(&p.part_lse[at(k)]).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ref = fmaxf(mx, -1e30f);
-    float wsum = 0.f, acc[2 * kC] = {};
-    for (int k0 = 0; k0 < ns; k0 += 32) {
-      const int k = k0 + lane;
-      const float2 ls = k < ns ? __ldcg(&p.part_lse[at(k)]) : make_float2(-INFINITY, 0.f);
-      const float w = exp2f(ls.x - ref), wo = w * ls.y;
-      wsum += w;
-      const int n = min(32, ns - k0);
-      for (int j0 = 0; j0 < n; j0 += 8) {
-        uint32_t ov[8][kC];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (j0 + u < n) {
-            const uint32_t* src = p.part_o + at(k0 + j0 + u) * (D / 2) + lane * kC;
-            if constexpr (kC == 2) {
-              const uint2 x = __ldcg(reinterpret_cast<const uint2*>(src));
-              ov[u][0] = x.x;
-              ov[u][1] = x.y;
-            } else {
-              ov[u][0] = __ldcg(src);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < kC; ++e) ov[u][e] = 0;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float wu = __shfl_sync(0xffffffffu, wo, j0 + u);
-#pragma unroll
-          for (int e = 0; e < kC; ++e) {
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&ov[u][e]));
-            acc[2 * e] = fmaf(wu, x.x, acc[2 * e]);
-            acc[2 * e + 1] = fmaf(wu, x.y, acc[2 * e + 1]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-    const int pr = row0 + row, tok = pr / p.G;
-    const int64_t orow = (int64_t)(r.q0 + tok) * p.Hq + s.g * p.G + pr - tok * p.G;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * kC;
-#pragma unroll
-    for (int e = 0; e < kC; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (p.lse && lane == 0)
-      p.lse[orow] = wsum > 0.f ? (ref + __log2f(wsum)) * 0.6931471805599453f : -INFINITY;
-  }
+  if (s.b >= 0)
+    merge_rows<D, kRows, kMergeWarps>(p, s, begin, begin + kMergeRows, threadIdx.x >> 5);
 }
 
 // ----------------------------------------------------------------- host
@@ -828,24 +763,21 @@ cudaError_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Params&
 }
 
 template <int D, int kRows>
-cudaError_t launch_merge(const Params& p, cudaStream_t stream) {
+cudaError_t launch_merge(const Params& p, int sms, cudaStream_t stream) {
   const int parts = (p.slot_rows + kMergeRows - 1) / kMergeRows;
-  cudaError_t e = launch_pdl(paged_merge_kernel<D, kRows>, dim3(p.max_ctas * parts),
+  cudaError_t e = launch_pdl(paged_merge_kernel<D, kRows>, dim3(sms * parts),
                              dim3(kMergeWarps * 32), 0, stream, p);
   note_launch();
   return e;
 }
-
-// CTAs whose partials a call keeps.
-int max_ctas(int64_t rows) { return (rows <= kFewRows ? 2 : 1) * num_sms(); }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
 size_t paged_attn_scratch_bytes(const PagedAttnArgs& a) {
-  const int64_t most = max_rows(a);
-  const size_t ctas = max_ctas(most), rows = (size_t)std::min<int64_t>(most, 2 * BM);
+  const size_t ctas = kFewBlocks * num_sms();
+  const size_t rows = (size_t)std::min<int64_t>(max_rows(a), 2 * BM);
   return align256(ctas * sizeof(Split)) + align256(2 * ctas * rows * sizeof(float2)) +
          2 * ctas * rows * a.p.head_dim * 2;
 }
@@ -868,25 +800,22 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   p.Hq = a.heads_q;
   p.G = a.heads_q / a.p.heads_kv;
   p.causal = a.causal ? 1 : 0;
-  p.max_ctas = max_ctas(rows);
+  p.inv_G = (uint32_t)((0x100000000ull + p.G - 1) / p.G);  // (unused where G = 1)
+  p.arrived = a.arrived;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   p.slot_rows = (int)std::min<int64_t>(rows, 2 * BM);
   uint8_t* s = static_cast<uint8_t*>(a.scratch);
   p.split = reinterpret_cast<Split*>(s);
-  s += align256(p.max_ctas * sizeof(Split));
+  s += align256((size_t)kFewBlocks * sms * sizeof(Split));
   p.part_lse = reinterpret_cast<float2*>(s);
-  s += align256((size_t)2 * p.max_ctas * p.slot_rows * sizeof(float2));
+  s += align256((size_t)2 * kFewBlocks * sms * p.slot_rows * sizeof(float2));
   p.part_o = reinterpret_cast<uint32_t*>(s);
   p.err = a.err;
   p.wait_ns = pipeline_wait_ns();
   p.stall = pipeline_test_stall() ? 1 : 0;
-  if (rows <= kFewRows) {
-    const cudaError_t e = launch_few(p, a.pool, (int)rows, sms, stream);
-    if (e != cudaSuccess) return e;
-    return D == 64 ? launch_merge<64, kFewRows>(p, stream) : launch_merge<128, kFewRows>(p, stream);
-  }
+  if (rows <= kFewRows) return launch_few(p, a.pool, (int)rows, sms, stream);
   CUtensorMap mk, mv;
   if (!encode_pages(&mk, a.pool.k, a.p, f8) || !encode_pages(&mv, a.pool.v, a.p, f8))
     return cudaErrorInvalidValue;
@@ -894,10 +823,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   auto go = [&](auto d, auto e4m3) {
     constexpr int kD = decltype(d)::value;
     constexpr bool k8 = decltype(e4m3)::value;
-    cudaError_t e = two ? launch_t<kD, k8, 2>(mk, mv, p, sms, stream)
-                        : launch_t<kD, k8, 1>(mk, mv, p, sms, stream);
+    const cudaError_t e = two ? launch_t<kD, k8, 2>(mk, mv, p, sms, stream)
+                              : launch_t<kD, k8, 1>(mk, mv, p, sms, stream);
     if (e != cudaSuccess) return e;
-    return two ? launch_merge<kD, 2 * BM>(p, stream) : launch_merge<kD, BM>(p, stream);
+    return two ? launch_merge<kD, 2 * BM>(p, sms, stream) : launch_merge<kD, BM>(p, sms, stream);
   };
   using std::integral_constant;
   using D64 = integral_constant<int, 64>;

@@ -42,6 +42,7 @@ namespace paged {
 namespace {
 
 constexpr int kFixed = 2;  // an item's overhead in key tiles
+constexpr int kMinShare = 4;
 constexpr float kLazy = 8.0f;
 
 // Warps per CTA and CTAs per SM by what a lane has to keep: 16 keys of data
@@ -51,7 +52,7 @@ template <int D, bool kF8, int NT>
 struct Few {
   static constexpr bool kSmall = kF8 ? NT == 1 : NT == 1 && D == 64;
   static constexpr int kWarps = kSmall ? 8 : NT == 1 ? 10 : 8;
-  static constexpr int kBlocks = kSmall ? 2 : 1;
+  static constexpr int kBlocks = kSmall ? kFewBlocks : 1;
   static constexpr int kRows = 8 * NT;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kLd = D + 4;  // floats per row of the merge area
@@ -122,10 +123,10 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
   const int g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_trigger();
-  find_share<F::kRows, kFixed, F::kThreads>(p, &share, warp_sums);
+  find_share<F::kRows, kFixed, kMinShare, F::kThreads>(p, &share, warp_sums);
   auto walk = start_walk<F::kRows, kFixed>(p, share);
   const int shift = p.b.page_shift, in_page = (1 << shift) - 1;
-  Seg sg;
+  Seg sg{};
   while (walk.next(p, sg)) {
     const int rows = sg.r.n * p.G;
     const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
-      const int tok = r / p.G;
+      const int tok = div_G(p, r);
       const __nv_bfloat16* src = p.q + (int64_t)(sg.r.q0 + min(tok, max(sg.r.n - 1, 0))) * p.q_stride +
                                  (int64_t)(sg.g * p.G + r - tok * p.G) * D;
       float mx = 0.f;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
       for (int u = 0; u < 2; ++u) {
         scale[nt][u] = __shfl_sync(0xffffffffu, mul, (2 * c + u) * 4);
         const int row = nt * 8 + 2 * c + u;
-        lim[nt][u] = row >= rows ? 0 : p.causal ? sg.r.len - sg.r.n + row / p.G + 1 : sg.r.len;
+        lim[nt][u] = row >= rows ? 0 : p.causal ? sg.r.len - sg.r.n + div_G(p, row) + 1 : sg.r.len;
       }
     }
     // ---- the keys of this warp: chunks of 16, every kWarps-th of the segment
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
 #pragma unroll
       for (int e = 0; e < kC; ++e) acc[e] *= inv;
       if (whole) {
-        const int tok = r / p.G;
+        const int tok = div_G(p, r);
         const int64_t at = (int64_t)(sg.r.q0 + tok) * p.Hq + sg.g * p.G + r - tok * p.G;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D) + lane * (kC / 2);
 #pragma unroll
@@ -411,11 +412,11 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) write_split<F::kRows, kFixed>(p, share);
+  finish_items<D, F::kRows, kFixed, F::kThreads>(p, share, sg);
 }
 
 template <int D, bool kF8, int NT>
-cudaError_t launch_t(Params& p, const PagedPool& pool, int sms, cudaStream_t stream) {
+cudaError_t launch_t(const Params& p, const PagedPool& pool, int sms, cudaStream_t stream) {
   using F = Few<D, kF8, NT>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
@@ -424,8 +425,7 @@ cudaError_t launch_t(Params& p, const PagedPool& pool, int sms, cudaStream_t str
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
   });
   if (attr != cudaSuccess) return attr;
-  p.max_ctas = F::kBlocks * sms;
-  cudaError_t e = launch_pdl(paged_few_kernel<D, kF8, NT>, dim3(p.max_ctas),
+  cudaError_t e = launch_pdl(paged_few_kernel<D, kF8, NT>, dim3(F::kBlocks * sms),
                              dim3(F::kThreads), F::kSmem, stream, p,
                              static_cast<const uint8_t*>(pool.k),
                              static_cast<const uint8_t*>(pool.v));
@@ -435,7 +435,7 @@ cudaError_t launch_t(Params& p, const PagedPool& pool, int sms, cudaStream_t str
 
 }  // namespace
 
-cudaError_t launch_few(Params& p, const PagedPool& pool, int rows, int sms,
+cudaError_t launch_few(const Params& p, const PagedPool& pool, int rows, int sms,
                        cudaStream_t stream) {
   const bool two = rows > 8;
   if (p.b.head_dim == 64) {
