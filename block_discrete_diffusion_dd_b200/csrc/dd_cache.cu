@@ -20,8 +20,10 @@
 // bf16's own exponent and mantissa bits give e without any floating-point
 // rounding.  E4M3 has no infinities: non-finite values are stored as NaN.
 //
-// Both are copies, bound by memory: a group of D / 8 lanes moves one (token,
-// head) row of K or V, 16 bytes of bf16 per lane.
+// Both are copies, bound by memory.  A unit is the row of one (token, K or V,
+// head); D / 8 lanes move it, 16 bytes of bf16 each.  A CTA takes N units per
+// lane group, all of their loads in flight at once, and looks its few tokens'
+// places up once, in shared memory; appending, the loads do not wait for that.
 #include "dd_paged.cuh"
 
 namespace dd {
@@ -29,8 +31,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Largest finite |x| of the 8 bf16 values in v, as bf16 bits.
+// Largest |x| of the 8 bf16 values in v, as bf16 bits (which order like the
+// magnitudes they stand for; 0x7f80 and above are infinities and NaN).
 __device__ __forceinline__ uint32_t amax_bits(uint4 v) {
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+  return max(m & 0xffffu, m >> 16);
+}
+// The same of the finite ones.
+__device__ __forceinline__ uint32_t amax_finite_bits(uint4 v) {
   uint32_t m = 0;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -40,6 +49,13 @@ __device__ __forceinline__ uint32_t amax_bits(uint4 v) {
     if (hi < 0x7f80u) m = max(m, hi);
   }
   return m;
+}
+// The largest of the values that the kLanes lanes of a row hold.
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_max(uint32_t a) {
+#pragma unroll
+  for (int off = kLanes / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+  return a;
 }
 
 // Scale byte (e + 127) for a largest magnitude given as bf16 bits: a =
@@ -51,10 +67,16 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t a) {
   return (uint32_t)max(s, 7);
 }
 
-// Four values as codes; `top` bounds their magnitudes (448, but 240 at the
-// largest exponent, 120, where the next code, 256, times 2^120 is no longer
-// a finite bf16 number).
-__device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, float inv, float top) {
+// Four values as codes.
+__device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, float inv) {
+  const float2 f = make_float2(inv, inv);
+  return pack_e4m3x4(__fmul2_rn(make_float2(bf16lo(a), bf16hi(a)), f),
+                     __fmul2_rn(make_float2(bf16lo(b), bf16hi(b)), f));
+}
+// Four values of a row with non-finite ones (NaN) or of the largest exponent,
+// where codes are bounded by 240: the next, 256, times 2^120 is no longer a
+// finite bf16 number.
+__device__ __forceinline__ uint32_t quant4_rare(uint32_t a, uint32_t b, float inv, float top) {
   float x[4] = {bf16lo(a) * inv, bf16hi(a) * inv, bf16lo(b) * inv, bf16hi(b) * inv};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -63,130 +85,224 @@ __device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, float inv, fl
   return pack_e4m3x4(make_float2(x[0], x[1]), make_float2(x[2], x[3]));
 }
 
-template <int D, bool kF8>
+// Where the units of a CTA start, and how a unit falls into (token, K or V,
+// head): units of a token are the heads of K, then the heads of V.
+template <int D, int N>
+struct Units {
+  static constexpr int kLanes = D / 8;
+  static constexpr int kGroups = kThreads / kLanes;  // units in one pass
+  static constexpr int kPer = kGroups * N;           // units of a CTA
+  static constexpr int kTokens = kPer / 2 + 1;       // the most tokens they touch
+};
+
+// From a unit to the one `units` further on, without a division each.
+struct Step {
+  int dt, dh, per;
+  __device__ __forceinline__ Step(int units, int per) : dt(units / per), dh(units % per), per(per) {}
+  __device__ __forceinline__ void operator()(int t, int h, int& t2, int& h2) const {
+    const bool over = h + dh >= per;
+    t2 = t + dt + (over ? 1 : 0);
+    h2 = h + dh - (over ? per : 0);
+  }
+};
+
+// Pool rows (head 0) of the CTA's tokens, -1 for those without a place.
+template <typename F>
+__device__ __forceinline__ void place_tokens(int64_t* rows, int first, int count, int total, F&& of) {
+  for (int k = threadIdx.x; k < count; k += kThreads)
+    rows[k] = first + k < total ? of(first + k) : -1;
+  __syncthreads();
+}
+
+template <int D, bool kF8, int N>
 __global__ void __launch_bounds__(kThreads)
     cache_append_kernel(const PagedBatch p, const uint16_t* __restrict__ k_new,
                         const uint16_t* __restrict__ v_new, int64_t k_stride, int64_t v_stride,
                         void* k_pool, void* v_pool, uint8_t* k_scale, uint8_t* v_scale,
                         uint32_t* err) {
-  constexpr int kLanes = D / 8;
+  using U = Units<D, N>;
+  __shared__ int64_t rows[U::kTokens];
   pdl_wait();
   pdl_trigger();
-  const int unit = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const int t = unit / (2 * p.heads_kv), hv = unit % (2 * p.heads_kv);
-  const int h = hv >> 1;
-  int64_t row = -1;
-  if (t < p.total_new) {
-    const int b = owner_row(p.cu_new, p.batch, t);
-    if (b >= 0) {
-      const ChunkRow c = chunk_row(p, b, err);
-      const int pos = c.len - c.n + (t - c.q0);
-      // (a row taken as empty has no position for its tokens)
-      if (t - c.q0 < c.n && pos >= 0) row = pool_row(p, b, pos, err);
+  const int H = p.heads_kv, l = threadIdx.x % U::kLanes;
+  const int u0 = blockIdx.x * U::kPer + threadIdx.x / U::kLanes;
+  const int first = blockIdx.x * U::kPer / (2 * H);
+  const Step step(U::kGroups, 2 * H);
+  uint4 v[N];
+  int tok[N], hv[N];
+  tok[0] = u0 / (2 * H);
+  hv[0] = u0 - tok[0] * 2 * H;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i > 0) step(tok[i - 1], hv[i - 1], tok[i], hv[i]);
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok[i] < p.total_new) {
+      const uint16_t* src = hv[i] < H ? k_new + tok[i] * k_stride + hv[i] * D
+                                      : v_new + tok[i] * v_stride + (hv[i] - H) * D;
+      v[i] = __ldg(reinterpret_cast<const uint4*>(src) + l);
     }
   }
-  const bool ok = row >= 0;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (ok) {
-    const uint16_t* src = (hv & 1) ? v_new + t * v_stride : k_new + t * k_stride;
-    v = *reinterpret_cast<const uint4*>(src + h * D + l * 8);
-    row += (int64_t)h << p.page_shift;
-  }
-  if constexpr (!kF8) {
-    if (ok) reinterpret_cast<uint4*>((hv & 1) ? v_pool : k_pool)[row * kLanes + l] = v;
-  } else {
-    uint32_t a = amax_bits(v);
+  place_tokens(rows, first, min(U::kTokens, (U::kPer - 1) / (2 * H) + 2), p.total_new, [&](int t) {
+    const int b = owner_row(p.cu_new, p.batch, t);
+    if (b < 0) return (int64_t)-1;
+    const ChunkRow c = chunk_row(p, b, err);
+    const int pos = c.len - c.n + (t - c.q0);
+    // (a row taken as empty has no position for its tokens)
+    return t - c.q0 < c.n && pos >= 0 ? pool_row(p, b, pos, err) : (int64_t)-1;
+  });
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1)
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
-    const uint32_t s = scale_byte(a);
-    const float inv = pow2f(127 - (int)s), top = s == 247u ? 240.f : 448.f;
-    if (ok) {
+  for (int i = 0; i < N; ++i) {
+    const bool is_v = hv[i] >= H;
+    int64_t row = rows[min(tok[i] - first, U::kTokens - 1)];
+    const bool ok = row >= 0 && tok[i] < p.total_new;
+    row += (int64_t)(is_v ? hv[i] - H : hv[i]) << p.page_shift;
+    if constexpr (!kF8) {
+      if (ok) reinterpret_cast<uint4*>(is_v ? v_pool : k_pool)[row * U::kLanes + l] = v[i];
+    } else {
+      const uint32_t a = row_max<U::kLanes>(amax_bits(v[i]));
+      uint32_t s = scale_byte(a);
       uint2 c;
-      c.x = quant4(v.x, v.y, inv, top);
-      c.y = quant4(v.z, v.w, inv, top);
-      reinterpret_cast<uint2*>((hv & 1) ? v_pool : k_pool)[row * kLanes + l] = c;
-      if (l == 0) ((hv & 1) ? v_scale : k_scale)[row] = (uint8_t)s;
+      // one comparison covers non-finite values and the largest exponent
+      if (!__any_sync(0xffffffffu, s >= 247u)) {
+        const float inv = pow2f(127 - (int)s);
+        c.x = quant4(v[i].x, v[i].y, inv);
+        c.y = quant4(v[i].z, v[i].w, inv);
+      } else {
+        s = scale_byte(row_max<U::kLanes>(amax_finite_bits(v[i])));
+        const float inv = pow2f(127 - (int)s), top = s == 247u ? 240.f : 448.f;
+        c.x = quant4_rare(v[i].x, v[i].y, inv, top);
+        c.y = quant4_rare(v[i].z, v[i].w, inv, top);
+      }
+      if (ok) {
+        reinterpret_cast<uint2*>(is_v ? v_pool : k_pool)[row * U::kLanes + l] = c;
+        if (l == 0) (is_v ? v_scale : k_scale)[row] = (uint8_t)s;
+      }
     }
   }
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, int N>
 __global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const PagedBatch p, const void* k_pool, const void* v_pool,
                       const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
                       uint4* __restrict__ k_out, uint4* __restrict__ v_out, uint32_t* err) {
-  constexpr int kLanes = D / 8;
+  using U = Units<D, N>;
+  __shared__ int64_t rows[U::kTokens];
   pdl_wait();
   pdl_trigger();
-  const int unit = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int l = threadIdx.x % kLanes;
-  const int t = unit / (2 * p.heads_kv), hv = unit % (2 * p.heads_kv);
-  const int h = hv >> 1;
-  if (t >= p.total_new) return;
-  const int b = owner_row(p.cu_new, p.batch, t);
-  if (b < 0) return;
-  const int pos = t - __ldg(p.cu_new + b);
-  if (pos >= (p.max_pages << p.page_shift)) {
-    atomicOr(err, kDevErrBounds);
-    return;
+  const int H = p.heads_kv, l = threadIdx.x % U::kLanes;
+  const int u0 = blockIdx.x * U::kPer + threadIdx.x / U::kLanes;
+  const int first = blockIdx.x * U::kPer / (2 * H);
+  place_tokens(rows, first, min(U::kTokens, (U::kPer - 1) / (2 * H) + 2), p.total_new, [&](int t) {
+    const int b = owner_row(p.cu_new, p.batch, t);
+    if (b < 0) return (int64_t)-1;
+    const int pos = t - __ldg(p.cu_new + b);
+    if (pos >= (p.max_pages << p.page_shift)) {
+      atomicOr(err, kDevErrBounds);
+      return (int64_t)-1;
+    }
+    return pool_row(p, b, pos, err);
+  });
+  uint4 v[N];
+  uint32_t sc[N];
+  int64_t out[N];  // output row, -1: none; complemented for V
+  bool ok[N];
+  const Step step(U::kGroups, 2 * H);
+  int tok = u0 / (2 * H), hv = u0 - tok * 2 * H;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i > 0) step(tok, hv, tok, hv);
+    const bool is_v = hv >= H;
+    const int h = is_v ? hv - H : hv;
+    int64_t row = rows[min(tok - first, U::kTokens - 1)];
+    ok[i] = row >= 0 && tok < p.total_new;
+    row += (int64_t)h << p.page_shift;
+    out[i] = (int64_t)tok * H + h;
+    if (is_v) out[i] = ~out[i];
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    sc[i] = 127;
+    if (ok[i]) {
+      const void* pool = is_v ? v_pool : k_pool;
+      if constexpr (kF8) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(pool) + row * U::kLanes + l);
+        v[i].x = c.x;
+        v[i].y = c.y;
+        sc[i] = __ldg((is_v ? v_scale : k_scale) + row);
+      } else {
+        v[i] = __ldg(reinterpret_cast<const uint4*>(pool) + row * U::kLanes + l);
+      }
+    }
   }
-  int64_t row = pool_row(p, b, pos, err);
-  if (row < 0) return;
-  row += (int64_t)h << p.page_shift;
-  uint4 o;
-  if constexpr (!kF8) {
-    o = reinterpret_cast<const uint4*>((hv & 1) ? v_pool : k_pool)[row * kLanes + l];
-  } else {
-    const uint2 c = reinterpret_cast<const uint2*>((hv & 1) ? v_pool : k_pool)[row * kLanes + l];
-    const float f = pow2f((int)((hv & 1) ? v_scale : k_scale)[row] - 127);
-    const float2 x0 = e4m3x2_to_float2(c.x), x1 = e4m3x2_to_float2(c.x >> 16);
-    const float2 x2 = e4m3x2_to_float2(c.y), x3 = e4m3x2_to_float2(c.y >> 16);
-    o = make_uint4(pack_bf16x2(x0.x * f, x0.y * f), pack_bf16x2(x1.x * f, x1.y * f),
-                   pack_bf16x2(x2.x * f, x2.y * f), pack_bf16x2(x3.x * f, x3.y * f));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (kF8) {
+      const float f = pow2f((int)sc[i] - 127);
+      const float2 x0 = e4m3x2_to_float2(v[i].x), x1 = e4m3x2_to_float2(v[i].x >> 16);
+      const float2 x2 = e4m3x2_to_float2(v[i].y), x3 = e4m3x2_to_float2(v[i].y >> 16);
+      v[i] = make_uint4(pack_bf16x2(x0.x * f, x0.y * f), pack_bf16x2(x1.x * f, x1.y * f),
+                        pack_bf16x2(x2.x * f, x2.y * f), pack_bf16x2(x3.x * f, x3.y * f));
+    }
+    const bool is_v = out[i] < 0;
+    if (ok[i]) __stcs((is_v ? v_out : k_out) + (is_v ? ~out[i] : out[i]) * U::kLanes + l, v[i]);
   }
-  ((hv & 1) ? v_out : k_out)[((int64_t)t * p.heads_kv + h) * kLanes + l] = o;
 }
 
-template <int D, bool kF8>
-cudaError_t append_t(const CacheAppendArgs& a, cudaStream_t stream) {
-  const int64_t units = (int64_t)a.p.total_new * 2 * a.p.heads_kv;
-  const int per = kThreads / (D / 8);
-  cudaError_t e = launch_pdl(cache_append_kernel<D, kF8>, dim3((unsigned)((units + per - 1) / per)),
-                             dim3(kThreads), 0, stream, a.p,
-                             static_cast<const uint16_t*>(a.k_new),
-                             static_cast<const uint16_t*>(a.v_new), a.k_stride, a.v_stride,
-                             a.pool.k, a.pool.v, a.pool.k_scale, a.pool.v_scale, a.err);
+// Units per lane group: as many as keep every SM busy.
+constexpr int kMany = 8;
+template <int D>
+bool many_units(int64_t units) {
+  return units >= (int64_t)Units<D, kMany>::kPer * 2 * 148;
+}
+
+template <int D, bool kF8, int N>
+cudaError_t append_t(const CacheAppendArgs& a, int64_t units, cudaStream_t stream) {
+  using U = Units<D, N>;
+  cudaError_t e = launch_pdl(
+      cache_append_kernel<D, kF8, N>, dim3((unsigned)((units + U::kPer - 1) / U::kPer)),
+      dim3(kThreads), 0, stream, a.p, static_cast<const uint16_t*>(a.k_new),
+      static_cast<const uint16_t*>(a.v_new), a.k_stride, a.v_stride, a.pool.k, a.pool.v,
+      a.pool.k_scale, a.pool.v_scale, a.err);
+  note_launch();
+  return e;
+}
+
+template <int D, bool kF8, int N>
+cudaError_t read_t(const CacheReadArgs& a, int64_t units, cudaStream_t stream) {
+  using U = Units<D, N>;
+  cudaError_t e = launch_pdl(
+      cache_read_kernel<D, kF8, N>, dim3((unsigned)((units + U::kPer - 1) / U::kPer)),
+      dim3(kThreads), 0, stream, a.p, (const void*)a.pool.k, (const void*)a.pool.v,
+      (const uint8_t*)a.pool.k_scale, (const uint8_t*)a.pool.v_scale,
+      static_cast<uint4*>(a.k_out), static_cast<uint4*>(a.v_out), a.err);
   note_launch();
   return e;
 }
 
 template <int D, bool kF8>
-cudaError_t read_t(const CacheReadArgs& a, cudaStream_t stream) {
+cudaError_t append_n(const CacheAppendArgs& a, cudaStream_t stream) {
   const int64_t units = (int64_t)a.p.total_new * 2 * a.p.heads_kv;
-  const int per = kThreads / (D / 8);
-  cudaError_t e = launch_pdl(cache_read_kernel<D, kF8>, dim3((unsigned)((units + per - 1) / per)),
-                             dim3(kThreads), 0, stream, a.p, (const void*)a.pool.k,
-                             (const void*)a.pool.v, (const uint8_t*)a.pool.k_scale,
-                             (const uint8_t*)a.pool.v_scale, static_cast<uint4*>(a.k_out),
-                             static_cast<uint4*>(a.v_out), a.err);
-  note_launch();
-  return e;
+  return many_units<D>(units) ? append_t<D, kF8, kMany>(a, units, stream)
+                              : append_t<D, kF8, 1>(a, units, stream);
+}
+template <int D, bool kF8>
+cudaError_t read_n(const CacheReadArgs& a, cudaStream_t stream) {
+  const int64_t units = (int64_t)a.p.total_new * 2 * a.p.heads_kv;
+  return many_units<D>(units) ? read_t<D, kF8, kMany>(a, units, stream)
+                              : read_t<D, kF8, 1>(a, units, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t stream) {
   if (a.p.head_dim == 64)
-    return a.pool.e4m3 ? append_t<64, true>(a, stream) : append_t<64, false>(a, stream);
-  return a.pool.e4m3 ? append_t<128, true>(a, stream) : append_t<128, false>(a, stream);
+    return a.pool.e4m3 ? append_n<64, true>(a, stream) : append_n<64, false>(a, stream);
+  return a.pool.e4m3 ? append_n<128, true>(a, stream) : append_n<128, false>(a, stream);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t stream) {
   if (a.p.head_dim == 64)
-    return a.pool.e4m3 ? read_t<64, true>(a, stream) : read_t<64, false>(a, stream);
-  return a.pool.e4m3 ? read_t<128, true>(a, stream) : read_t<128, false>(a, stream);
+    return a.pool.e4m3 ? read_n<64, true>(a, stream) : read_n<64, false>(a, stream);
+  return a.pool.e4m3 ? read_n<128, true>(a, stream) : read_n<128, false>(a, stream);
 }
 
 }  // namespace dd
