@@ -11,14 +11,17 @@
 // as the target's own samples.
 //
 // Four kernels:
-//   scan    one read of all the target's rows: per chunk of kScan logits the
-//           maximum and the sum of 2^((x - max) c), c = log2(e) / tau, in
-//           fp32 (c as two floats, so that the long argument of a small term
-//           does not lose what its many peers add up to).  Bound by memory.
+//   scan    one read of all the target's rows: per chunk of 1,024 16-byte
+//           blocks a reference r and the sum of 2^(x c - r), c = log2(e) / tau,
+//           in fp32.  Bound by memory, with the exponentials close behind (one
+//           per entry: 23 us of MUFU time against 30 us of HBM time for 390
+//           bf16 rows of 262,144).
 //   decide  one CTA per sequence merges the chunks of its rows, forms p(x_i)
-//           in 64 bits and takes the first refusal.  A test within kNear of
-//           equality is repeated with a 64-bit sum over the row, so that the
-//           decision is the one exact arithmetic takes.
+//           and takes the first refusal.  A test within kNear of equality is
+//           repeated with a 64-bit sum over the row, so that the decision is
+//           the one exact arithmetic takes: the fp32 exponents are off by at
+//           most 2^-24 |x c| and c by 2^-25 of itself, which moves p by less
+//           than 1e-6 for scores within 30 of each other.
 //   norm    for the one row the next token is drawn at: the 64-bit sums of
 //           the target's and the draft's exponentials per chunk of kPick
 //           logits.  The running sum has a border per vocabulary entry (up
@@ -27,16 +30,19 @@
 //           a hundred would land on another token, with 64 bits none does.
 //   pick    the weights' sums per chunk; the last chunk to finish finds the
 //           chunk that holds u_s W and walks it.
-// Sums are taken in a fixed order, so a call's result does not depend on
-// scheduling.
+// The last three are latency: each thread asks for all it needs at once, and a
+// phase is one or two barriers.  Sums are taken in a fixed order, so a call's
+// result does not depend on scheduling.
 #include "dd_paged.cuh"
 
 namespace dd {
 namespace {
 
-constexpr int kScan = 8192;  // logits per scan chunk
-constexpr int kPick = 2048;  // logits per norm / pick chunk
 constexpr int kThreads = 256;
+constexpr int kBlocks = 4;               // 16-byte blocks of a thread of the scan
+constexpr int kPer = 8;                  // entries of a thread of norm and pick
+constexpr int kPick = kThreads * kPer;   // logits per norm / pick chunk
+constexpr int kDecideThreads = 1024;
 constexpr double kNear = 1e-5;
 
 // What `decide` hands on about sequence b's draw.
@@ -63,7 +69,7 @@ struct VerifyParams {
   const float *u_accept, *u_sample;
   int32_t *accepted, *tokens;
   float* target_prob;
-  float2* scan;       // [total + batch][scan chunks]: maximum, sum
+  float2* scan;       // [total + batch][scan chunks]: reference, sum
   uint8_t* state;     // [total]: 0 accepted, 1 refused, 2 near
   Draw* draw;         // [batch]
   Part* part;         // [batch][2][pick chunks]
@@ -88,68 +94,160 @@ __device__ __forceinline__ F warp_sum(F v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Block-wide sum / maximum in every thread (a fixed order; 2 barriers).
-template <typename F>
-__device__ F block_sum(F v, F* sm) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+// Block-wide maxima of two values, or sums of two, in every thread (the sums
+// in a fixed order).  `sm` is not reused before the next barrier.
+struct Pair {
+  double x, y;
+};
+__device__ __forceinline__ float2 block_max2(float x, float y, float2* sm) {
+  x = warp_max(x);
+  y = warp_max(y);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float2(x, y);
   __syncthreads();
-  F r = 0;
+  float2 r = sm[0];
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) r += sm[i];
-  __syncthreads();
+  for (int i = 1; i < kThreads / 32; ++i) r = make_float2(fmaxf(r.x, sm[i].x), fmaxf(r.y, sm[i].y));
   return r;
 }
-__device__ float block_max(float v, float* sm) {
-  v = warp_max(v);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+__device__ __forceinline__ Pair block_sum2(double x, double y, Pair* sm) {
+  x = warp_sum(x);
+  y = warp_sum(y);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = Pair{x, y};
   __syncthreads();
-  float r = sm[0];
+  Pair r{0, 0};
 #pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) r = fmaxf(r, sm[i]);
-  __syncthreads();
+  for (int i = 0; i < kThreads / 32; ++i) {
+    r.x += sm[i].x;
+    r.y += sm[i].y;
+  }
   return r;
 }
 
 // A maximum that exponents may be taken against: rows (chunks) of -inf only
 // get a finite one, against which every term is 0.
-__device__ __forceinline__ float safe_max(float m) { return fmaxf(m, -3.0e38f); }
+__device__ __forceinline__ float safe_max(float m) { return fmaxf(m, -1.0e30f); }
 
+// Entries of a 16-byte block as floats.
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 v, float (&x)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      x[2 * i] = bf16lo(w[i]);
+      x[2 * i + 1] = bf16hi(w[i]);
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+// The largest entry of some blocks: packed comparisons for bf16.
+template <typename T>
+__device__ __forceinline__ float blocks_max(const uint4 (&v)[kBlocks]) {
+  if constexpr (sizeof(T) == 2) {
+    auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    __nv_bfloat162 m = h(v[0].x);
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+      m = __hmax2(m, __hmax2(__hmax2(h(v[i].x), h(v[i].y)), __hmax2(h(v[i].z), h(v[i].w))));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+      m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y))),
+                fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w)));
+    return m;
+  }
+}
+
+// A row is read in aligned 16-byte blocks, whatever its start; entries of the
+// first and the last block that are not the row's count as -inf.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_scan_kernel(const VerifyParams p, int chunks) {
-  __shared__ float smf[kThreads / 32];
+  constexpr int kE = 16 / sizeof(T);
+  __shared__ float2 sm[kThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x / chunks, ch = blockIdx.x % chunks;
   const T* x = static_cast<const T*>(p.target) + row * p.target_stride;
-  const int v0 = ch * kScan, v1 = min(p.vocab, v0 + kScan);
-  float m = -INFINITY;
-  for (int v = v0 + threadIdx.x; v < v1; v += kThreads) m = fmaxf(m, logit(x, v));
-  m = block_max(m, smf);
-  const float mr = safe_max(m), c = (float)p.c, c_lo = (float)(p.c - (double)c);
-  float s = 0.f;
-  for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-    const float d = logit(x, v) - mr;
-    s += ex2_approx(fmaf(d, c, d * c_lo));
+  const int skew = (int)(reinterpret_cast<uintptr_t>(x) & 15u) / (int)sizeof(T);
+  const uint4* base = reinterpret_cast<const uint4*>(x - skew);
+  const int blocks = (p.vocab + skew + kE - 1) / kE;
+  const bool whole = (p.vocab + skew) % kE == 0;  // the last block is all the row's
+  const int b0 = ch * kThreads * kBlocks + threadIdx.x;
+  uint4 v[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    const int b = b0 + i * kThreads;
+    constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+    v[i] = make_uint4(kNone, kNone, kNone, kNone);
+    if ((b > 0 || skew == 0) && (b < blocks - 1 || (b == blocks - 1 && whole))) {
+      v[i] = __ldcs(base + b);
+    } else if (b < blocks) {  // an end of the row: entry by entry
+      uint32_t w[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int at = b * kE + e - skew;
+        if (at < 0 || at >= p.vocab) continue;
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t bits = __ldg(x + at);
+          w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (bits << 16) : (w[e / 2] & 0xffff0000u) | bits;
+        } else {
+          w[e] = __ldg(x + at);
+        }
+      }
+      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  s = block_sum(s, smf);
-  if (threadIdx.x == 0) p.scan[(int64_t)row * chunks + ch] = make_float2(m, s);
+  // each warp has a reference of its own
+  const float c = (float)p.c;
+  const float ref = safe_max(warp_max(blocks_max<T>(v))) * c;
+  const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+  float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    float e[kE];
+    unpack<T>(v[i], e);
+#pragma unroll
+    for (int k = 0; k < kE; k += 2) {
+      const float2 d = __ffma2_rn(make_float2(e[k], e[k + 1]), c2, r2);
+      s2 = __fadd2_rn(s2, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
+    }
+  }
+  const float s = warp_sum(s2.x + s2.y);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float2(ref, s);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float top = sm[0].x, sum = 0.f;
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) top = fmaxf(top, sm[i].x);
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) sum = fmaf(sm[i].y, exp2f(sm[i].x - top), sum);
+    p.scan[(int64_t)row * chunks + ch] = make_float2(top, sum);
+  }
 }
 
-// p(x) of one row with 64-bit sums (the whole CTA; the near-tie path).
+// p(x) of one row with 64-bit sums relative to 2^ref (the whole CTA; the
+// near-tie path).
 template <typename T>
-__device__ double exact_prob(const T* x, int vocab, double c, float m, int tok, double* smd) {
+__device__ double exact_prob(const T* x, int vocab, double c, double ref, int tok, double* smd) {
   double s = 0;
-  for (int v = threadIdx.x; v < vocab; v += kThreads)
-    s += exp2(((double)logit(x, v) - (double)m) * c);
-  s = block_sum(s, smd);
-  return exp2(((double)logit(x, tok) - (double)m) * c) / s;
+  for (int v = threadIdx.x; v < vocab; v += kDecideThreads) s += exp2((double)logit(x, v) * c - ref);
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) smd[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0;
+  for (int i = 0; i < kDecideThreads / 32; ++i) s += smd[i];
+  __syncthreads();
+  return exp2((double)logit(x, tok) * c - ref) / s;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kDecideThreads)
     verify_decide_kernel(const VerifyParams p, int chunks) {
-  __shared__ double smd[kThreads / 32];
+  __shared__ double smd[kDecideThreads / 32];
   __shared__ int first;
   pdl_wait();
   pdl_trigger();
@@ -168,33 +266,30 @@ __global__ void __launch_bounds__(kThreads)
   auto row_of = [&](int i) {
     return static_cast<const T*>(p.target) + (int64_t)(q0 + b + i) * p.target_stride;
   };
-  auto row_max = [&](int i) {  // the row's maximum, in every lane
+  // the row's reference and sum, from its chunks, in every lane
+  auto merge = [&](int i, float& ref) {
     const float2* sc = p.scan + (int64_t)(q0 + b + i) * chunks;
-    float m = -INFINITY;
-    for (int c = lane; c < chunks; c += 32) m = fmaxf(m, sc[c].x);
-    return safe_max(warp_max(m));
+    const float2 mine = lane < chunks ? sc[lane] : make_float2(-INFINITY, 0.f);
+    ref = mine.x;
+    for (int c = lane + 32; c < chunks; c += 32) ref = fmaxf(ref, sc[c].x);
+    ref = warp_max(ref);
+    double s = (double)mine.y * exp2f(mine.x - ref);
+    for (int c = lane + 32; c < chunks; c += 32) s += (double)sc[c].y * exp2f(sc[c].x - ref);
+    return warp_sum(s);
   };
-  for (int i = warp; i < k; i += kThreads / 32) {
-    const float2* sc = p.scan + (int64_t)(q0 + b + i) * chunks;
-    const float m = row_max(i);
-    double s = 0;
-    for (int c = lane; c < chunks; c += 32)
-      s += (double)sc[c].y * exp2(((double)safe_max(sc[c].x) - (double)m) * p.c);
-    s = warp_sum(s);
+  const float c1 = (float)p.c;  // the scan's own factor
+  for (int i = warp; i < k; i += kDecideThreads / 32) {
+    const int tok = p.draft_tokens[q0 + i];
+    const double bar = (double)p.u_accept[q0 + i] * (double)p.draft_conf[q0 + i];
+    const bool in = (uint32_t)tok < (uint32_t)p.vocab;
+    const float x = in ? logit(row_of(i), tok) : -INFINITY;
+    float ref;
+    const double s = merge(i, ref);
     if (lane == 0) {
-      const int tok = p.draft_tokens[q0 + i];
-      double pr = 0;
-      uint8_t st = 1;
-      if ((uint32_t)tok >= (uint32_t)p.vocab) {
-        atomicOr(p.err, kDevErrBounds);
-      } else {
-        if (s > 0) pr = exp2(((double)logit(row_of(i), tok) - (double)m) * p.c) / s;
-        const double bar = (double)p.u_accept[q0 + i] * (double)p.draft_conf[q0 + i];
-        st = fabs(bar - pr) <= kNear * pr ? 2 : bar < pr ? 0 : 1;
-        if (pr == 0) st = 1;
-      }
+      if (!in) atomicOr(p.err, kDevErrBounds);
+      const double pr = s > 0 ? exp2((double)x * (double)c1 - (double)ref) / s : 0;
       p.target_prob[q0 + i] = (float)pr;
-      p.state[q0 + i] = st;
+      p.state[q0 + i] = pr == 0 ? 1 : fabs(bar - pr) <= kNear * pr ? 2 : bar < pr ? 0 : 1;
     }
   }
   __syncthreads();
@@ -202,7 +297,7 @@ __global__ void __launch_bounds__(kThreads)
   while (true) {  // the first row that is not accepted; near ones are decided in 64 bits
     if (threadIdx.x == 0) first = k;
     __syncthreads();
-    for (int i = n + threadIdx.x; i < k; i += kThreads)
+    for (int i = n + threadIdx.x; i < k; i += kDecideThreads)
       if (p.state[q0 + i] != 0) {
         atomicMin(&first, i);
         break;
@@ -211,12 +306,13 @@ __global__ void __launch_bounds__(kThreads)
     n = first;
     __syncthreads();
     if (n == k || p.state[q0 + n] == 1) break;
-    const float m = row_max(n);
-    const double pr = exact_prob(row_of(n), p.vocab, p.c, m, p.draft_tokens[q0 + n], smd);
+    float ref;
+    merge(n, ref);
+    const double pr = exact_prob(row_of(n), p.vocab, p.c, (double)ref, p.draft_tokens[q0 + n], smd);
     if (!((double)p.u_accept[q0 + n] * (double)p.draft_conf[q0 + n] < pr)) break;
     ++n;
   }
-  for (int i = threadIdx.x; i <= k; i += kThreads)
+  for (int i = threadIdx.x; i <= k; i += kDecideThreads)
     if (i != n) p.tokens[q0 + b + i] = i < n ? p.draft_tokens[q0 + i] : -1;
   if (threadIdx.x == 0) {
     p.accepted[b] = n;
@@ -227,193 +323,236 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Maximum and 64-bit sum of one chunk of a row (the whole CTA).
+// This thread's kPer consecutive entries of a chunk: bits of one or two
+// 16-byte loads where the row is aligned, entry by entry where not.
 template <typename T>
-__device__ Part chunk_part(const T* x, int v0, int v1, double c, float* smf, double* smd) {
-  float m = -INFINITY;
-  for (int v = v0 + threadIdx.x; v < v1; v += kThreads) m = fmaxf(m, logit(x, v));
-  Part r;
-  r.m = safe_max(block_max(m, smf));
-  double s = 0;
-  for (int v = v0 + threadIdx.x; v < v1; v += kThreads)
-    s += exp2(((double)logit(x, v) - (double)r.m) * c);
-  r.s = block_sum(s, smd);
-  r.pad = 0;
-  return r;
+__device__ __forceinline__ void load_entries(const T* x, int v0, int vocab, float (&e)[kPer]) {
+  constexpr int kE = 16 / sizeof(T);
+  if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0 && v0 + kPer <= vocab) {
+#pragma unroll
+    for (int i = 0; i < kPer / kE; ++i) {
+      float f[kE];
+      unpack<T>(__ldg(reinterpret_cast<const uint4*>(x + v0) + i), f);
+#pragma unroll
+      for (int k = 0; k < kE; ++k) e[i * kE + k] = f[k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = v0 + i < vocab ? logit(x, v0 + i) : -INFINITY;
+  }
+}
+
+// What the target's row and the draft's (if any) hold at the draw of b.
+template <typename T>
+__device__ __forceinline__ void load_rows(const VerifyParams& p, const Draw& dr, int ch,
+                                          float (&xt)[kPer], float (&xd)[kPer]) {
+  const int v0 = ch * kPick + threadIdx.x * kPer;
+  load_entries(static_cast<const T*>(p.target) + dr.t_row * p.target_stride, v0, p.vocab, xt);
+  if (dr.d_row >= 0)
+    load_entries(static_cast<const T*>(p.draft) + dr.d_row * p.draft_stride, v0, p.vocab, xd);
+  else
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) xd[i] = -INFINITY;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_norm_kernel(const VerifyParams p, int chunks) {
-  __shared__ float smf[kThreads / 32];
-  __shared__ double smd[kThreads / 32];
+  __shared__ float2 smf[kThreads / 32];
+  __shared__ Pair smd[kThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / chunks, ch = blockIdx.x % chunks;
   const Draw dr = p.draw[b];
   if (dr.out < 0) return;
-  const int v0 = ch * kPick, v1 = min(p.vocab, v0 + kPick);
-  Part* part = p.part + (int64_t)b * 2 * chunks + ch;
-  const Part a = chunk_part(static_cast<const T*>(p.target) + dr.t_row * p.target_stride, v0, v1,
-                            p.c, smf, smd);
-  if (threadIdx.x == 0) part[0] = a;
-  if (dr.d_row >= 0) {
-    const Part d = chunk_part(static_cast<const T*>(p.draft) + dr.d_row * p.draft_stride, v0, v1,
-                              p.cd, smf, smd);
-    if (threadIdx.x == 0) part[chunks] = d;
+  float xt[kPer], xd[kPer];
+  load_rows<T>(p, dr, ch, xt, xd);
+  float mt = xt[0], md = xd[0];
+#pragma unroll
+  for (int i = 1; i < kPer; ++i) {
+    mt = fmaxf(mt, xt[i]);
+    md = fmaxf(md, xd[i]);
   }
-}
-
-// Maximum and sum of a whole row from its chunks (the whole CTA).
-__device__ Part row_part(const Part* part, int chunks, double c, float* smf, double* smd) {
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < chunks; i += kThreads) m = fmaxf(m, part[i].m);
-  Part r;
-  r.m = safe_max(block_max(m, smf));
-  double s = 0;
-  for (int i = threadIdx.x; i < chunks; i += kThreads)
-    s += part[i].s * exp2(((double)part[i].m - (double)r.m) * c);
-  r.s = block_sum(s, smd);
-  r.pad = 0;
-  return r;
+  float2 m = block_max2(mt, md, smf);
+  m = make_float2(safe_max(m.x), safe_max(m.y));
+  double st = 0, sd = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) st += exp2(((double)xt[i] - (double)m.x) * p.c);
+  if (dr.d_row >= 0)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sd += exp2(((double)xd[i] - (double)m.y) * p.cd);
+  const Pair s = block_sum2(st, sd, smd);
+  if (threadIdx.x == 0) {
+    Part* part = p.part + (int64_t)b * 2 * chunks + ch;
+    part[0] = Part{s.x, m.x, 0};
+    part[chunks] = Part{s.y, m.y, 0};
+  }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParams p, int chunks) {
-  __shared__ float smf[kThreads / 32];
-  __shared__ double smd[kThreads / 32];
-  __shared__ int s_last, s_chunk, s_tok, s_any;
-  __shared__ double s_before;
-  constexpr int kPer = kPick / kThreads;
+  __shared__ float2 smf[kThreads / 32];
+  __shared__ Pair smd[3][kThreads / 32];
+  __shared__ int s_last, s_chunk, s_tok;
+  __shared__ double s_bar;
+  constexpr int kWarps = kThreads / 32;
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / chunks, ch = blockIdx.x % chunks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Draw dr = p.draw[b];
   if (dr.out < 0) return;
+  const bool drafted = dr.d_row >= 0;
+  float xt[kPer], xd[kPer];
+  load_rows<T>(p, dr, ch, xt, xd);
+  // both rows' maxima and sums from the chunks'
   const Part* part = p.part + (int64_t)b * 2 * chunks;
-  const T* xt = static_cast<const T*>(p.target) + dr.t_row * p.target_stride;
-  const T* xd = static_cast<const T*>(p.draft) + max(dr.d_row, 0) * p.draft_stride;
-  const Part zt = row_part(part, chunks, p.c, smf, smd);
-  Part zd{};
-  if (dr.d_row >= 0) zd = row_part(part + chunks, chunks, p.cd, smf, smd);
-  const double it = zt.s > 0 ? 1.0 / zt.s : 0.0, id = zd.s > 0 ? 1.0 / zd.s : 0.0;
-  // weight of entry v; `rest`: the residual rather than the target itself
-  auto weight = [&](int v, bool rest) {
-    double w = exp2(((double)logit(xt, v) - (double)zt.m) * p.c) * it;
-    if (rest) w = fmax(w - exp2(((double)logit(xd, v) - (double)zd.m) * p.cd) * id, 0.0);
-    return w;
-  };
-  // consecutive entries per thread, so that a walk in thread order is one
-  // in vocabulary order
-  auto thread_sum = [&](int c, bool rest, double (&w)[kPer]) {
+  const Part none{0, -INFINITY, 0};
+  const Part pt = (int)threadIdx.x < chunks ? part[threadIdx.x] : none;
+  const Part pd = (int)threadIdx.x < chunks ? part[chunks + threadIdx.x] : none;
+  float mt = pt.m, md = pd.m;
+  for (int i = threadIdx.x + kThreads; i < chunks; i += kThreads) {
+    mt = fmaxf(mt, part[i].m);
+    md = fmaxf(md, part[chunks + i].m);
+  }
+  const float2 m = block_max2(mt, md, smf);
+  double st = pt.s * exp2(((double)pt.m - (double)m.x) * p.c);
+  double sd = pd.s * exp2(((double)pd.m - (double)m.y) * p.cd);
+  for (int i = threadIdx.x + kThreads; i < chunks; i += kThreads) {
+    st += part[i].s * exp2(((double)part[i].m - (double)m.x) * p.c);
+    sd += part[chunks + i].s * exp2(((double)part[chunks + i].m - (double)m.y) * p.cd);
+  }
+  const Pair z = block_sum2(st, sd, smd[0]);
+  const double it = z.x > 0 ? 1.0 / z.x : 0.0, id = z.y > 0 ? 1.0 / z.y : 0.0;
+  // this thread's weights in a chunk whose logits are loaded (-inf: 0), and
+  // their sum; consecutive entries per thread, so that thread order is
+  // vocabulary order
+  auto weigh = [&](bool rest, double (&w)[kPer]) {
     double s = 0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      const int v = c * kPick + threadIdx.x * kPer + e;
-      w[e] = v < p.vocab ? weight(v, rest) : 0.0;
+      w[e] = exp2(((double)xt[e] - (double)m.x) * p.c) * it;
+      if (rest) w[e] = fmax(w[e] - exp2(((double)xd[e] - (double)m.y) * p.cd) * id, 0.0);
       s += w[e];
     }
     return s;
   };
   double w[kPer];
-  bool rest = dr.d_row >= 0;
-  const double ws = block_sum(thread_sum(ch, rest, w), smd);
+  const double ws = block_sum2(weigh(drafted, w), 0, smd[1]).x;
   double* weights = p.weight + (int64_t)b * chunks;
   if (threadIdx.x == 0) {
     weights[ch] = ws;
     __threadfence();
     s_last = atomicAdd(&p.draw[b].arrived, 1) == chunks - 1;
+    __threadfence();
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
-  // every chunk's sum is there: find the chunk, then the entry
-  if (threadIdx.x == 0) {
-    double total = 0;
-    for (int i = 0; i < chunks; ++i) total += __ldcg(weights + i);
-    if (!(total > 0) && rest) {  // no residual mass: the target itself
-      rest = false;
-      total = 0;
-      for (int i = 0; i < chunks; ++i) {
-        weights[i] = part[i].s * exp2(((double)part[i].m - (double)zt.m) * p.c) * it;
-        total += weights[i];
-      }
+  // every chunk's sum is there: this CTA finds the chunk, then the entry.
+  // A scan of per-thread sums of `n` consecutive values: exclusive prefix.
+  auto prefix = [&](double mine, Pair* sm, double& total) {
+    double inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
     }
-    const double bar = (double)p.u_sample[b] * total;
-    int pick = -1;
-    double run = 0, before = 0;
-    for (int i = 0; i < chunks; ++i) {
-      const double wi = __ldcg(weights + i);
-      if (wi > 0) {  // the last chunk with mass, unless an earlier one passes the bar
-        pick = i;
-        before = run;
-      }
-      run += wi;
-      if (run > bar) break;
+    __syncthreads();
+    if (lane == 31) sm[warp].x = inc;
+    if (threadIdx.x == 0) {
+      s_chunk = -1;
+      s_tok = p.vocab;
     }
-    s_chunk = pick;
-    s_before = bar - before;
-    s_any = rest ? 1 : 0;
-    s_tok = p.vocab;
+    __syncthreads();
+    double before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += sm[i].x;
+      total += sm[i].x;
+    }
+    return before + inc - mine;
+  };
+  const int each = (chunks + kThreads - 1) / kThreads;  // chunks of a thread
+  bool rest = drafted;
+  double total = 0, at = 0;
+  auto chunk_weight = [&](int i) {
+    return rest || !drafted ? __ldcg(weights + i)
+                            : part[i].s * exp2(((double)part[i].m - (double)m.x) * p.c) * it;
+  };
+  while (true) {
+    double mine = 0;
+    for (int i = threadIdx.x * each; i < min(chunks, (int)(threadIdx.x + 1) * each); ++i)
+      mine += chunk_weight(i);
+    at = prefix(mine, smd[2], total);
+    if (total > 0 || !rest) break;
+    rest = false;  // no residual mass: the target itself
   }
+  const double bar = (double)p.u_sample[b] * total;
+  // the first chunk that passes the bar; none does (rounding): the last with
+  // mass.  Its thread keeps the weight before it.
+  int pass = -1, mass = -1;
+  double before_pass = 0, before_mass = 0;
+  for (int i = threadIdx.x * each; i < min(chunks, (int)(threadIdx.x + 1) * each); ++i) {
+    const double wi = chunk_weight(i);
+    if (wi > 0) {
+      mass = i;
+      before_mass = at;
+      if (pass < 0 && at + wi > bar) {
+        pass = i;
+        before_pass = at;
+      }
+    }
+    at += wi;
+  }
+  if (pass >= 0) atomicMin(&s_tok, pass);
+  if (mass >= 0) atomicMax(&s_chunk, mass);
   __syncthreads();
-  const int c = s_chunk;
+  const int c = s_tok < p.vocab ? s_tok : s_chunk;
   if (c < 0) {  // no mass at all: every logit of the target's row is -inf
     if (threadIdx.x == 0) p.tokens[dr.out] = -1;
     return;
   }
-  double run = thread_sum(c, s_any != 0, w);
-  // exclusive prefix over the threads, in a fixed order
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  double inc = run;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double up = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += up;
-  }
-  if (lane == 31) smd[warp] = inc;
-  __syncthreads();
-  double at = inc - run;
-  for (int i = 0; i < warp; ++i) at += smd[i];
+  if (c == pass) s_bar = bar - before_pass;
+  else if (c == mass && s_tok == p.vocab) s_bar = bar - before_mass;
+  load_rows<T>(p, dr, c, xt, xd);
+  double sum;
+  at = prefix(weigh(rest, w), smd[2], sum);  // (its barriers publish s_bar)
   int last = -1;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    const int v = c * kPick + threadIdx.x * kPer + e;
     at += w[e];
     if (w[e] > 0) {
-      last = v;
-      if (at > s_before) {
-        atomicMin(&s_tok, v);
+      last = c * kPick + threadIdx.x * kPer + e;
+      if (at > s_bar) {
+        atomicMin(&s_tok, last);
         break;
       }
     }
   }
-  __syncthreads();
-  const int tok = s_tok;
-  __syncthreads();
-  if (tok < p.vocab) {
-    if (threadIdx.x == 0) p.tokens[dr.out] = tok;
-    return;
-  }
-  // rounding left the bar at the chunk's end: its last entry with mass
-  if (threadIdx.x == 0) s_chunk = -1;
-  __syncthreads();
   if (last >= 0) atomicMax(&s_chunk, last);
   __syncthreads();
-  if (threadIdx.x == 0) p.tokens[dr.out] = s_chunk;
+  // (rounding may leave the bar at the chunk's end: its last entry with mass)
+  if (threadIdx.x == 0) p.tokens[dr.out] = s_tok < p.vocab ? s_tok : s_chunk;
 }
 
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
-int scan_chunks(int vocab) { return (vocab + kScan - 1) / kScan; }
+// (one entry short of a block more than the row has, for any alignment)
+template <typename T>
+int scan_chunks(int vocab) {
+  constexpr int kE = 16 / sizeof(T), kChunk = kThreads * kBlocks * kE;
+  return (int)(((int64_t)vocab + kE - 1 + kChunk - 1) / kChunk);
+}
 int pick_chunks(int vocab) { return (vocab + kPick - 1) / kPick; }
 
 template <typename T>
 cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
-  const int sc = scan_chunks(p.vocab), pc = pick_chunks(p.vocab);
+  const int sc = scan_chunks<T>(p.vocab), pc = pick_chunks(p.vocab);
   cudaError_t e = launch_pdl(verify_scan_kernel<T>, dim3((p.total + p.batch) * sc), dim3(kThreads),
                              0, stream, p, sc);
   note_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(verify_decide_kernel<T>, dim3(p.batch), dim3(kThreads), 0, stream, p, sc);
+  e = launch_pdl(verify_decide_kernel<T>, dim3(p.batch), dim3(kDecideThreads), 0, stream, p,
+                 sc);
   note_launch();
   if (e != cudaSuccess) return e;
   e = launch_pdl(verify_norm_kernel<T>, dim3(p.batch * pc), dim3(kThreads), 0, stream, p, pc);
@@ -427,7 +566,7 @@ cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t verify_scratch_bytes(int batch, int total, int vocab) {
-  const size_t sc = scan_chunks(vocab), pc = pick_chunks(vocab);
+  const size_t sc = scan_chunks<uint32_t>(vocab), pc = pick_chunks(vocab);  // fp32: the more
   return align16((size_t)(total + batch) * sc * sizeof(float2)) + align16((size_t)total) +
          align16((size_t)batch * sizeof(Draw)) + (size_t)batch * 2 * pc * sizeof(Part) +
          (size_t)batch * pc * sizeof(double);
@@ -453,7 +592,7 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   p.tokens = a.tokens;
   p.target_prob = a.target_prob;
   p.err = a.err;
-  const size_t sc = scan_chunks(a.vocab), pc = pick_chunks(a.vocab);
+  const size_t sc = scan_chunks<uint32_t>(a.vocab), pc = pick_chunks(a.vocab);
   uint8_t* s = static_cast<uint8_t*>(a.scratch);
   p.scan = reinterpret_cast<float2*>(s);
   s += align16((size_t)(a.total + a.batch) * sc * sizeof(float2));
