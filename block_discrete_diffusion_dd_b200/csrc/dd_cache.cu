@@ -237,10 +237,13 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < N; ++i) {
     if constexpr (kF8) {
       const float f = pow2f((int)sc[i] - 127);
-      const float2 x0 = e4m3x2_to_float2(v[i].x), x1 = e4m3x2_to_float2(v[i].x >> 16);
-      const float2 x2 = e4m3x2_to_float2(v[i].y), x3 = e4m3x2_to_float2(v[i].y >> 16);
-      v[i] = make_uint4(pack_bf16x2(x0.x * f, x0.y * f), pack_bf16x2(x1.x * f, x1.y * f),
-                        pack_bf16x2(x2.x * f, x2.y * f), pack_bf16x2(x3.x * f, x3.y * f));
+      const float2 ff = make_float2(f, f);
+      const uint2 a = e4m3x4_to_f16(v[i].x), b = e4m3x4_to_f16(v[i].y);
+      auto pair = [&](uint32_t h) {
+        const float2 x = __fmul2_rn(f16x2_to_float2(h), ff);
+        return pack_bf16x2(x.x, x.y);
+      };
+      v[i] = make_uint4(pair(a.x), pair(a.y), pair(b.x), pair(b.y));
     }
     const bool is_v = out[i] < 0;
     if (ok[i]) __stcs((is_v ? v_out : k_out) + (is_v ? ~out[i] : out[i]) * U::kLanes + l, v[i]);

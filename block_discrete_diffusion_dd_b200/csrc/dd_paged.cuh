@@ -60,10 +60,19 @@ __device__ __forceinline__ int64_t pool_row(const PagedBatch& p, int b, int pos,
 // 2^e as a float, e in [-126, 127].
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((127 + e) << 23); }
 
-// Two E4M3 bytes (low byte first) as floats; exact, NaN stays NaN.
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  return __half22float2(__half2(h));
+// Four E4M3 bytes (lowest first) as two fp16 pairs; exact, NaN stays NaN.
+__device__ __forceinline__ uint2 e4m3x4_to_f16(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 }  // namespace dd

@@ -129,12 +129,16 @@ __device__ __forceinline__ void issue_pv(uint32_t dO, uint32_t aP, uint64_t bv, 
 // 16 E4M3 codes (16 bytes) times f as bf16.
 __device__ __forceinline__ void expand16(uint4 c, float f, uint4& lo, uint4& hi) {
   const float2 ff = make_float2(f, f);
-  auto pair = [&](uint32_t w) {
-    const float2 x = __fmul2_rn(e4m3x2_to_float2(w), ff);
-    return pack_bf16x2(x.x, x.y);
+  auto four = [&](uint32_t w, uint32_t& a, uint32_t& b) {
+    const uint2 h = e4m3x4_to_f16(w);
+    const float2 x = __fmul2_rn(f16x2_to_float2(h.x), ff), y = __fmul2_rn(f16x2_to_float2(h.y), ff);
+    a = pack_bf16x2(x.x, x.y);
+    b = pack_bf16x2(y.x, y.y);
   };
-  lo = make_uint4(pair(c.x), pair(c.x >> 16), pair(c.y), pair(c.y >> 16));
-  hi = make_uint4(pair(c.z), pair(c.z >> 16), pair(c.w), pair(c.w >> 16));
+  four(c.x, lo.x, lo.y);
+  four(c.y, lo.z, lo.w);
+  four(c.z, hi.x, hi.y);
+  four(c.w, hi.z, hi.w);
 }
 
 template <int D, bool kF8, int kQT>

@@ -98,12 +98,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Two E4M3 codes (the low or high half of w) as fp16, exact.
-__device__ __forceinline__ uint32_t f16_of(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-
 template <int D, bool kF8, int NT>
 __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kBlocks)
     paged_few_kernel(const Params p, const uint8_t* __restrict__ k_pool,
@@ -192,55 +186,78 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
     const int32_t* table = p.b.page_table + (int64_t)sg.b * p.b.max_pages;
     const int first = sg.t0 * (BN / 16) + warp;
     const int last = min(sg.t1 * (BN / 16), cdiv(sg.r.len, 16));  // chunks end
-    // pool row of position 16 i + 8 h (its 8 keys share a page), or -1
-    auto look = [&](int i, int h) -> int64_t {
-      const int pos = i * 16 + h * 8;
-      if (i >= last || pos >= sg.r.len) return -1;
-      const int page = __ldg(table + (pos >> shift));
+    // The 8 keys from position 16 i + 8 h on share a page: where they start in
+    // the pools, in bytes, and the last of them that exists.  Behind the
+    // sequence's end its last key stands in, whose weight is then 0: loads
+    // need no condition, and what lies past the end is not read.
+    struct Place {
+      int64_t at;
+      int most;
+    };
+    const int end8 = (sg.r.len - 1) & ~7;
+    auto page_of = [&](int i, int h) { return __ldg(table + (min(i * 16 + h * 8, end8) >> shift)); };
+    auto place_of = [&](int i, int h, int page) {
+      const int pos = min(i * 16 + h * 8, end8);
       if ((uint32_t)page >= (uint32_t)p.b.num_pages) {
         atomicOr(p.err, kDevErrBounds);
-        return -1;
+        page = 0;
       }
-      return (((int64_t)page * p.b.heads_kv + sg.g) << shift) + (pos & in_page);
+      const int64_t row = (((int64_t)page * p.b.heads_kv + sg.g) << shift) + (pos & in_page);
+      return Place{row, min(7, sg.r.len - 1 - pos)};
     };
-    uint4 kd[2][kJ];                              // keys g, g + 8
-    uint4 vd[4][(kVB + 15) / 16];                 // keys 2c, 2c + 1, 2c + 8, 2c + 9
-    float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};  // scale exponents of keys g, g + 8
-    auto load_k = [&](int i, const int64_t (&row)[2]) {
+    uint4 kd[2][kJ];               // keys g, g + 8
+    uint4 vd[4][(kVB + 15) / 16];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    uint32_t ks[2], vs[2];         // scale bytes of keys g, g + 8
+    auto load_k = [&](const Place (&pl)[2]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool ok = row[h] >= 0 && i * 16 + h * 8 + g < sg.r.len;
+        const int64_t row = pl[h].at + min(g, pl[h].most);
+        const uint8_t* src = k_pool + row * kRow + c * 16;
 #pragma unroll
-        for (int j = 0; j < kJ; ++j)
-          kd[h][j] = ok ? ld16(k_pool + (row[h] + g) * kRow + j * 64 + c * 16)
-                        : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < kJ; ++j) kd[h][j] = ld16(src + j * 64);
         if constexpr (kF8) {
-          ks[h] = ok ? (float)((int)__ldg(p.k_scale + row[h] + g) - 127) : 0.f;
-          vs[h] = ok ? (float)((int)__ldg(p.v_scale + row[h] + g) - 127) : 0.f;
+          ks[h] = __ldg(p.k_scale + row);
+          vs[h] = __ldg(p.v_scale + row);
         }
       }
     };
-    auto load_v = [&](int i, const int64_t (&row)[2]) {
+    auto load_v = [&](const Place (&pl)[2]) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int h = u >> 1, key = 2 * c + (u & 1);
-        const bool ok = row[h] >= 0 && i * 16 + h * 8 + key < sg.r.len;
-        const uint8_t* src = v_pool + (row[h] + key) * kRow + g * kVB;
-        if constexpr (kVB >= 16) {
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* src = v_pool + pl[h].at * kRow + g * kVB;
 #pragma unroll
-          for (int e = 0; e < kVB / 16; ++e)
-            vd[u][e] = ok ? ld16(src + e * 16) : make_uint4(0u, 0u, 0u, 0u);
-        } else {
-          const uint2 x = ok ? ld8(src) : make_uint2(0u, 0u);
-          vd[u][0] = make_uint4(x.x, x.y, 0u, 0u);
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* at = src + min(2 * c + u, pl[h].most) * kRow;
+          if constexpr (kVB >= 16) {
+#pragma unroll
+            for (int e = 0; e < kVB / 16; ++e) vd[2 * h + u][e] = ld16(at + e * 16);
+          } else {
+            const uint2 x = ld8(at);
+            vd[2 * h + u][0] = make_uint4(x.x, x.y, 0u, 0u);
+          }
         }
       }
     };
-    int64_t row[2] = {look(first, 0), look(first, 1)};
-    load_k(first, row);
-    load_v(first, row);
+    // page ids are asked for two chunks ahead, keys and values one
+    Place place[2];
+    int page[2] = {0, 0};
+    if (first < last) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) place[h] = place_of(first, h, page_of(first, h));
+      load_k(place);
+      load_v(place);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) page[h] = page_of(first + F::kWarps, h);
+    }
     for (int i = first; i < last; i += F::kWarps) {
-      const int64_t nrow[2] = {look(i + F::kWarps, 0), look(i + F::kWarps, 1)};
+      const bool more = i + F::kWarps < last;
+      if (more) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          place[h] = place_of(i + F::kWarps, h, page[h]);
+          page[h] = page_of(i + 2 * F::kWarps, h);
+        }
+      }
       // ---- S^T: keys g, g + 8 by query rows 2c, 2c + 1
       float s[NT][4] = {};
 #pragma unroll
@@ -251,10 +268,11 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
         for (int x = 0; x < kKS; ++x) {
           uint32_t a0, a1, a2, a3;
           if constexpr (kF8) {
-            a0 = f16_of(a[x]);
-            a2 = f16_of(a[x] >> 16);
-            a1 = f16_of(b[x]);
-            a3 = f16_of(b[x] >> 16);
+            const uint2 h0 = e4m3x4_to_f16(a[x]), h1 = e4m3x4_to_f16(b[x]);
+            a0 = h0.x;
+            a2 = h0.y;
+            a1 = h1.x;
+            a3 = h1.y;
           } else {
             a0 = a[2 * x];
             a2 = a[2 * x + 1];
@@ -268,18 +286,20 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
           }
         }
       }
-      const float ek[2] = {ks[0], ks[1]}, ev[2] = {vs[0], vs[1]};
-      load_k(i + F::kWarps, nrow);  // in flight over the rest of this chunk
-      // ---- softmax
-      float fk[2], fv[2];
+      // 2^ek, ev and 2^-ev of keys g, g + 8
+      float fk[2], ev[2], fv[2];
+      if constexpr (kF8) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        fk[h] = kF8 ? pow2f((int)ek[h]) : 1.f;
-        fv[h] = kF8 ? pow2f(-(int)ev[h]) : 1.f;
+        for (int h = 0; h < 2; ++h) {
+          fk[h] = __uint_as_float(ks[h] << 23);
+          ev[h] = __uint_as_float(0x4b000000u + vs[h]) - (8388608.f + 127.f);  // 2^23 + byte
+          fv[h] = __uint_as_float((254u - vs[h]) << 23);
+        }
       }
+      if (more) load_k(place);  // in flight over the rest of this chunk
+      // ---- softmax
       uint32_t wf[NT][2];
       bool grow = false;
-      float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -287,23 +307,20 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
           const int h = e >> 1, u = e & 1;
           const float x = kF8 ? fmaf(s[nt][e], fk[h] * scale[nt][u], ev[h]) : s[nt][e] * scale[nt][u];
           s[nt][e] = i * 16 + h * 8 + g < lim[nt][u] ? x : -INFINITY;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float v = fmaxf(s[nt][u], s[nt][2 + u]);
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          mx[nt][u] = v;
-          grow |= v > m[nt][u] + kLazy;
+          grow |= s[nt][e] > m[nt][u] + kLazy;
         }
       }
+      // the reference moves only when a score passes it by a margin
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float mn = fmaxf(m[nt][u], mx[nt][u]);
+            float mn = fmaxf(s[nt][u], s[nt][2 + u]);
+            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 4));
+            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
+            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
+            mn = fmaxf(m[nt][u], mn);
             const float al = ex2_approx(m[nt][u] - mn);
             m[nt][u] = mn;
             l[nt][u] *= al;
@@ -328,26 +345,39 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
                                      : pack_bf16x2(w[2 * h], w[2 * h + 1]));
       }
       // ---- O^T
+      auto word = [&](int u, int i) {  // 32-bit word i of key u's columns
+        const uint4& q = vd[u][i >> 2];
+        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+      };
+      if constexpr (kF8) {
 #pragma unroll
-      for (int t = 0; t < kMT; ++t) {
-        uint32_t h[4];
+        for (int t = 0; t < kMT; t += 2) {  // four columns: codes of two keys paired, then expanded
+          uint32_t w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if constexpr (kF8) {
-            const uint4& q = vd[u][0];
-            const uint32_t word = (t >> 1) == 0 ? q.x : (t >> 1) == 1 ? q.y : (t >> 1) == 2 ? q.z : q.w;
-            h[u] = f16_of((t & 1) ? word >> 16 : word);
-          } else {
-            const uint4& q = vd[u][t >> 2];
-            h[u] = (t & 3) == 0 ? q.x : (t & 3) == 1 ? q.y : (t & 3) == 2 ? q.z : q.w;
+          for (int u = 0; u < 4; ++u) w[u] = word(u, t >> 1);
+          const uint2 a = e4m3x4_to_f16(__byte_perm(w[0], w[1], 0x5140));
+          const uint2 b = e4m3x4_to_f16(__byte_perm(w[2], w[3], 0x5140));
+          const uint2 c2 = e4m3x4_to_f16(__byte_perm(w[0], w[1], 0x7362));
+          const uint2 d = e4m3x4_to_f16(__byte_perm(w[2], w[3], 0x7362));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<kF8>(o[nt][t], a.x, a.y, b.x, b.y, wf[nt][0], wf[nt][1]);
+            mma<kF8>(o[nt][t + 1], c2.x, c2.y, d.x, d.y, wf[nt][0], wf[nt][1]);
           }
         }
-        const uint32_t a0 = __byte_perm(h[0], h[1], 0x5410), a1 = __byte_perm(h[0], h[1], 0x7632);
-        const uint32_t a2 = __byte_perm(h[2], h[3], 0x5410), a3 = __byte_perm(h[2], h[3], 0x7632);
+      } else {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma<kF8>(o[nt][t], a0, a1, a2, a3, wf[nt][0], wf[nt][1]);
+        for (int t = 0; t < kMT; ++t) {
+          uint32_t w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[u] = word(u, t);
+          const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
+          const uint32_t a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma<kF8>(o[nt][t], a0, a1, a2, a3, wf[nt][0], wf[nt][1]);
+        }
       }
-      load_v(i + F::kWarps, nrow);
+      if (more) load_v(place);
     }
     // ---- this warp's rows into the merge area
 #pragma unroll
