@@ -82,23 +82,28 @@ template <int D, bool kF8, int kQT>
 struct Lay {
   static constexpr uint32_t kTile = BM * D * 2;  // a bf16 operand tile
   static constexpr uint32_t kRaw = BN * D;       // an E4M3 tile
-  static constexpr int kStages = D == 128 ? (kQT == 1 && !kF8 ? 3 : 2) : 4;
-  static constexpr int kRawStages = kF8 ? (kQT == 1 ? 4 : 2) : 0;
+  // 8-bit caches: with two query tiles one expanded K tile suffices (the next
+  // one is expanded while the softmax works), which leaves room for three 8-bit
+  // tiles in flight
+  static constexpr int kStagesK = D == 64 ? 4 : kF8 ? 3 - kQT : 4 - kQT;
+  static constexpr int kStagesV = D == 64 ? 4 : 2;
+  static constexpr int kRawStages = !kF8 ? 0 : D == 64 ? 4 : 3;
   static constexpr int kSoftWarps = 8 * kQT;
-  static constexpr int kConvWarps = kF8 ? (kQT == 1 ? 8 : 2) : 0;
+  static constexpr int kConvWarps = kF8 ? 6 : 0;
   static constexpr int kWarpTMA = kSoftWarps, kWarpMMA = kSoftWarps + 1;
   static constexpr int kThreads = (kSoftWarps + 2 + kConvWarps) * 32;
   static constexpr uint32_t kOffK = kQT * kTile;
-  static constexpr uint32_t kOffV = kOffK + kStages * kTile;
-  static constexpr uint32_t kOffRaw = kOffV + kStages * kTile;
+  static constexpr uint32_t kOffV = kOffK + kStagesK * kTile;
+  static constexpr uint32_t kOffRaw = kOffV + kStagesV * kTile;
   static constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRaw;
   static constexpr uint32_t kOffBar = kOffScale + kRawStages * BN;
   static constexpr uint32_t kSmem = kOffBar + sizeof(Barriers) + 1024;
   // an item's overhead (its Q tile, first product and epilogue) in key tiles
   static constexpr int kFixed = kQT == 1 ? 2 : 3;
   static constexpr int kMinShare = kFixed;
-  static_assert(kStages <= kMaxStages && kRawStages <= kMaxRaw, "barrier arrays");
-  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kStagesK <= kMaxStages && kStagesV <= kMaxStages && kRawStages <= kMaxRaw,
+                "barrier arrays");
+  static_assert(kSmem + 3072 <= 232448, "shared memory budget, static part included");
 };
 
 __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t off) {
@@ -156,10 +161,12 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
   volatile int* abort_flag = &bars->abort;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
+    for (int i = 0; i < L::kStagesK; ++i) {
       mbar_init(&bars->k_full[i], kF8 ? L::kConvWarps : 1);
-      mbar_init(&bars->v_full[i], kF8 ? L::kConvWarps : 1);
       mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kStagesV; ++i) {
+      mbar_init(&bars->v_full[i], kF8 ? L::kConvWarps : 1);
       mbar_init(&bars->v_empty[i], 1);
     }
     for (int i = 0; i < L::kRawStages; ++i) {
@@ -190,214 +197,25 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  auto walk = start_walk<kQT * BM, L::kFixed>(p, share);
-  const bool work = walk.pos < walk.end;
-  Seg sg{};
+  // Each warp walks the share by itself; the walk's state lies in shared memory,
+  // since the softmax has no registers to spare for it.
+  __shared__ Walk<kQT * BM, L::kFixed> walks[L::kThreads / 32];
+  __shared__ Seg segs[L::kThreads / 32];
+  const bool work = share.pos < share.end;
+  const Seg& sg = segs[warp];
+  if (lane == 0) {
+    walks[warp] = start_walk<kQT * BM, L::kFixed>(p, share);
+    segs[warp] = Seg{};
+  }
+  auto next = [&]() {
+    bool got = false;
+    __syncwarp();
+    if (lane == 0) got = walks[warp].next(p, segs[warp]);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
+  };
 
-  if (warp == L::kWarpTMA) {
-    // ------------------------------------------------------------ TMA
-    // Lane l < 16 looks up the page of the tile's 8-key group l, and issues
-    // the copy where that group starts a page (or the tile).
-    int tile = 0;  // tiles issued
-    const int ps = 1 << p.b.page_shift, per = min(ps, BN);
-    if (lane == 0 && work) {
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
-    }
-    bool ok = true;
-    while (ok && walk.next(p, sg)) {
-      const int32_t* table = p.b.page_table + (int64_t)sg.b * p.b.max_pages;
-      auto look = [&](int t) {
-        const int pos = t * BN + lane * 8;
-        return lane < BN / 8 && t < sg.t1 && pos < sg.r.len
-                   ? __ldg(table + (pos >> p.b.page_shift)) : -1;
-      };
-      int page = look(sg.t0);
-      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++tile) {
-        const int after = look(t + 1);
-        const int pos = t * BN + lane * 8;
-        const bool live = lane < BN / 8 && pos < sg.r.len;
-        int at = page;
-        if (live && (uint32_t)page >= (uint32_t)p.b.num_pages) {
-          atomicOr(p.err, kDevErrBounds);
-          at = p.b.num_pages;  // outside the tensor map: read as zero
-        }
-        const bool lead = live && (lane * 8) % per == 0;
-        const uint32_t bytes =
-            (uint32_t)__popc(__ballot_sync(0xffffffffu, lead)) * per * D * (kF8 ? 1 : 2);
-        const int c1 = pos & (ps - 1) & ~(per - 1), c2 = at * p.b.heads_kv + sg.g;
-        for (int v = 0; v < 2 && ok; ++v) {
-          const CUtensorMap* map = v ? &tmV : &tmK;
-          uint64_t *full, *empty;
-          uint8_t* dst;
-          int round;
-          if constexpr (kF8) {
-            const int n = 2 * tile + v, st = n % L::kRawStages;
-            round = n / L::kRawStages;
-            full = &bars->raw_full[st];
-            empty = &bars->raw_empty[st];
-            dst = smem + L::kOffRaw + st * L::kRaw;
-          } else {
-            const int st = tile % L::kStages;
-            round = tile / L::kStages;
-            full = v ? &bars->v_full[st] : &bars->k_full[st];
-            empty = v ? &bars->v_empty[st] : &bars->k_empty[st];
-            dst = smem + (v ? L::kOffV : L::kOffK) + st * L::kTile;
-          }
-          if (round > 0)
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait_bounded(empty, (round - 1) & 1, abort_flag, p.wait_ns));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-          __syncwarp();
-          if constexpr (kF8) {
-            if (lead) tma_load_3d(dst + lane * 8 * D, map, full, 0, c1, c2);
-            if (lane < BN / 8) {
-              if (live && at == page) {
-                const int64_t row = ((int64_t)c2 << p.b.page_shift) + (pos & (ps - 1));
-                uint8_t* sc = smem + L::kOffScale + ((2 * tile + v) % L::kRawStages) * BN;
-                cp_async8(sc + lane * 8, (v ? p.v_scale : p.k_scale) + row);
-              }
-              cp_async_arrive(full);
-            }
-          } else if (lead) {
-#pragma unroll
-            for (int a = 0; a < D / 64; ++a)
-              tma_load_3d(dst + a * kAtom + lane * 8 * 128, map, full, a * 64, c1, c2);
-          }
-          __syncwarp();
-        }
-        page = after;
-      }
-    }
-    if (lane == 0) write_split<L::kFixed>(p, share, sg);
-    // copies still in flight must land before the CTA exits (all have, unless
-    // the CTA gave up: then the last tiles' barriers are waited for, those of
-    // copies that were not issued any more running out)
-    if (*abort_flag) {
-      for (int n = max(0, tile - kMaxStages); n <= tile; ++n)
-        for (int v = 0; v < 2; ++v) {
-          const int i = 2 * n + v;
-          uint64_t* full = kF8 ? &bars->raw_full[i % max(1, L::kRawStages)]
-                           : v ? &bars->v_full[n % L::kStages] : &bars->k_full[n % L::kStages];
-          const int round = kF8 ? i / max(1, L::kRawStages) : n / L::kStages;
-          mbar_wait_bounded(full, round & 1, nullptr, kDrainNs / 64);
-        }
-    }
-    __syncwarp();
-  } else if (warp == L::kWarpMMA) {
-    // ------------------------------------------------------------ MMA
-    const bool leader = elect_one_sync();
-    const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t dK = smem_desc_sw128(smem_u32(smem + L::kOffK), 16, 1024);
-    const uint64_t dV = smem_desc_sw128(smem_u32(smem + L::kOffV), kAtom, 1024);
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool r = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns));
-      tc_fence_after();
-      return r;
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (leader) tc_commit(bar);
-      __syncwarp();
-    };
-    int kt = 0, vt = 0;             // K and V tiles consumed
-    int pcnt[2] = {0, 0};           // P tiles consumed per buffer
-    int segs[2] = {0, 0};           // segments per query tile
-    int sbuf = 0, pbuf = 0;         // kQT = 1: the next S / P buffer
-    bool ok = true, first = true;
-    // S of key tile kt for query tile q (all of them share the K stage)
-    auto s_tile = [&](int nq) {
-      const int st = kt % L::kStages;
-      if (!wait(&bars->k_full[st], (kt / L::kStages) & 1)) return false;
-      for (int q = 0; q < nq; ++q) {
-        const int buf = kQT == 1 ? sbuf : q;
-        if (leader) {
-          issue_s<D>(tmem + buf * BN, desc_at(dQ, q * L::kTile), desc_at(dK, st * L::kTile));
-          tc_commit(&bars->s_full[buf]);
-        }
-        __syncwarp();
-      }
-      sbuf ^= 1;
-      commit(&bars->k_empty[st]);
-      ++kt;
-      return true;
-    };
-    while (ok && walk.next(p, sg)) {
-      const int n = sg.t1 - sg.t0;
-      if (n == 0) continue;
-      const int rows = sg.r.n * p.G - sg.tp * kQT * BM;
-      const int nq = kQT == 1 ? 1 : min(kQT, cdiv(rows, BM));
-      for (int q = 0; q < nq && ok; ++q) ok = wait(&bars->q_full[q], segs[q] & 1);
-      if (!ok) break;
-      // the first products
-      if (!(ok = s_tile(nq))) break;
-      if (kQT == 1 && n > 1 && !(ok = s_tile(1))) break;
-      if (first && p.stall && !(ok = wait(&bars->never, 0))) break;
-      first = false;
-      for (int j = 0; j < n && ok; ++j) {
-        const int vst = vt % L::kStages;
-        if (!(ok = wait(&bars->v_full[vst], (vt / L::kStages) & 1))) break;
-        if constexpr (!kF8) {
-          // V rows past the sequence's length: zero, whatever the page holds
-          const int valid = sg.r.len - (sg.t0 + j) * BN;
-          if (valid < BN) {
-            uint8_t* v = smem + L::kOffV + vst * L::kTile;
-            for (int i = lane; i < (BN - valid) * 8; i += 32)
-#pragma unroll
-              for (int a = 0; a < D / 64; ++a)
-                *reinterpret_cast<uint4*>(v + a * kAtom + valid * 128 + i * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        const uint64_t bv = desc_at(dV, vst * L::kTile);
-        // the next product: tile j + 1 for two query tiles (interleaved with
-        // the P.V products), tile j + 2 for one
-        const bool more = j + (kQT == 1 ? 2 : 1) < n;
-        const int kst = kt % L::kStages;
-        for (int q = 0; q < nq; ++q) {
-          const int buf = kQT == 1 ? pbuf : q;
-          if (!(ok = wait(&bars->p_full[buf], pcnt[buf] & 1))) break;
-          ++pcnt[buf];
-          if (leader)
-            issue_pv<D>(tmem + kTmemO + q * D, tmem + buf * BN, bv, j > 0);
-          __syncwarp();
-          if (kQT == 1) {
-            commit(&bars->pv_done);
-          } else if (more) {
-            if (q == 0 && !(ok = wait(&bars->k_full[kst], (kt / L::kStages) & 1))) break;
-            if (leader) {
-              issue_s<D>(tmem + q * BN, desc_at(dQ, q * L::kTile), desc_at(dK, kst * L::kTile));
-              tc_commit(&bars->s_full[q]);
-            }
-            __syncwarp();
-          }
-        }
-        if (!ok) break;
-        pbuf ^= 1;
-        commit(&bars->v_empty[vst]);
-        ++vt;
-        if (more) {
-          if (kQT == 1) {
-            if (!(ok = s_tile(1))) break;
-          } else {
-            commit(&bars->k_empty[kst]);
-            ++kt;
-          }
-        }
-      }
-      if (!ok) break;
-      for (int q = 0; q < nq; ++q) {
-        commit(&bars->o_done[q]);
-        ++segs[q];
-      }
-    }
-    // every MMA issued above has completed before TMEM is released
-    commit(&bars->mma_final);
-    mbar_wait_bounded(&bars->mma_final, 0, nullptr, kDrainNs);
-    __syncwarp();
-  } else if (warp < L::kSoftWarps) {
+  if (warp < L::kSoftWarps) {
     // ------------------------------------------------------------ softmax
     const int q = warp >> 3, wl = warp & 3, hv = (warp >> 2) & 1;
     const int t4 = lane & 3;
@@ -418,7 +236,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       v += __shfl_xor_sync(0xffffffffu, v, 1);
       return v + __shfl_xor_sync(0xffffffffu, v, 2);
     };
-    while (ok && walk.next(p, sg)) {
+    while (ok && next()) {
       const int row0 = (sg.tp * kQT + q) * BM;         // packed row of the tile's row 0
       const int rows = sg.r.n * p.G - row0;            // valid rows of this tile
       if (rows <= 0) continue;
@@ -486,25 +304,36 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
         if (active) {
           tc_fence_after();
           const int k0 = (sg.t0 + j) * BN;
-          uint32_t sv[64];
-          tmem_ld16x256b_x16(tS, sv);
-          if (k0 + BN > full_to) {
-            const int vA = limA - k0, vB = limB - k0;
+          // The scores in kH parts of 128 / kH columns: with an 8-bit cache and
+          // two query tiles 24 warps leave 80 registers each, and the upper
+          // half is loaded twice, first for the maximum, then for P, whose
+          // columns by then only overlie scores that are used up.
+          constexpr int kH = kF8 && kQT == 2 ? 2 : 1, kI = 16 / kH;
+          uint32_t sv[4 * kI];
+          auto load = [&](int h) {
+            if constexpr (kH == 1) tmem_ld16x256b_x16(tS, sv);
+            else tmem_ld16x256b_x8(tS + (uint32_t)(h * 64), sv);
+            if (k0 + BN > full_to) {
+              const int vA = limA - k0 - h * 64, vB = limB - k0 - h * 64;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int c = 8 * i + 2 * t4;
-              if (c >= vA) sv[4 * i] = __float_as_uint(-INFINITY);
-              if (c + 1 >= vA) sv[4 * i + 1] = __float_as_uint(-INFINITY);
-              if (c >= vB) sv[4 * i + 2] = __float_as_uint(-INFINITY);
-              if (c + 1 >= vB) sv[4 * i + 3] = __float_as_uint(-INFINITY);
+              for (int i = 0; i < kI; ++i) {
+                const int c = 8 * i + 2 * t4;
+                if (c >= vA) sv[4 * i] = __float_as_uint(-INFINITY);
+                if (c + 1 >= vA) sv[4 * i + 1] = __float_as_uint(-INFINITY);
+                if (c >= vB) sv[4 * i + 2] = __float_as_uint(-INFINITY);
+                if (c + 1 >= vB) sv[4 * i + 3] = __float_as_uint(-INFINITY);
+              }
             }
-          }
-          float ma = fmaxf(__uint_as_float(sv[0]), __uint_as_float(sv[1]));
-          float mb = fmaxf(__uint_as_float(sv[2]), __uint_as_float(sv[3]));
+          };
+          float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
-          for (int i = 1; i < 16; ++i) {
-            ma = fmaxf(ma, fmaxf(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])));
-            mb = fmaxf(mb, fmaxf(__uint_as_float(sv[4 * i + 2]), __uint_as_float(sv[4 * i + 3])));
+          for (int h = kH - 1; h >= 0; --h) {
+            load(h);
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              ma = fmaxf(ma, fmaxf(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])));
+              mb = fmaxf(mb, fmaxf(__uint_as_float(sv[4 * i + 2]), __uint_as_float(sv[4 * i + 3])));
+            }
           }
           const float xa = quad_max(ma) * p.scale_log2, xb = quad_max(mb) * p.scale_log2;
           if (j == 0) {
@@ -540,22 +369,27 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
           }
           const float2 na = make_float2(-mrefA, -mrefA), nb = make_float2(-mrefB, -mrefB);
           float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
-          uint32_t w[32];  // 16x128b: w[2i] row A, w[2i + 1] row B, column 4 i + t % 4
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 da = __ffma2_rn(
-                make_float2(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])), sl2, na);
-            const float2 db = __ffma2_rn(
-                make_float2(__uint_as_float(sv[4 * i + 2]), __uint_as_float(sv[4 * i + 3])), sl2,
-                nb);
-            const float2 pa = make_float2(ex2_approx(da.x), ex2_approx(da.y));
-            const float2 pb = make_float2(ex2_approx(db.x), ex2_approx(db.y));
-            sa = __fadd2_rn(sa, pa);
-            sb = __fadd2_rn(sb, pb);
-            w[2 * i] = pack_bf16x2(pa.x, pa.y);
-            w[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
+          for (int h = 0; h < kH; ++h) {
+            if (h > 0) load(h);
+            uint32_t w[2 * kI];  // 16x128b: w[2i] row A, w[2i + 1] row B, column 4 i + t % 4
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              const float2 da = __ffma2_rn(
+                  make_float2(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])), sl2, na);
+              const float2 db = __ffma2_rn(
+                  make_float2(__uint_as_float(sv[4 * i + 2]), __uint_as_float(sv[4 * i + 3])), sl2,
+                  nb);
+              const float2 pa = make_float2(ex2_approx(da.x), ex2_approx(da.y));
+              const float2 pb = make_float2(ex2_approx(db.x), ex2_approx(db.y));
+              sa = __fadd2_rn(sa, pa);
+              sb = __fadd2_rn(sb, pb);
+              w[2 * i] = pack_bf16x2(pa.x, pa.y);
+              w[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
+            }
+            if constexpr (kH == 1) tmem_st16x128b_x16(tS, w);
+            else tmem_st16x128b_x8(tS + (uint32_t)(h * 32), w);
           }
-          tmem_st16x128b_x16(tS, w);
           lA += sa.x + sa.y;
           lB += sb.x + sb.y;
           tmem_wait_st();
@@ -578,9 +412,6 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       const float invA = lrowA > 0.f ? 1.f / lrowA : 0.f, invB = lrowB > 0.f ? 1.f / lrowB : 0.f;
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (sg.t0 > 0 ? 0 : 1);
-      uint32_t o[D / 2];
-      if constexpr (D == 128) tmem_ld16x256b_x16(tO, o);
-      else tmem_ld16x256b_x8(tO, o);
       float sA = invA, sB = invB;
       int eA = 0, eB = 0;
       if (!whole) {
@@ -589,10 +420,15 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
         // maximum in half the bytes of fp32
         float mA = 0.f, mB = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          mA = fmaxf(mA, fmaxf(fabsf(__uint_as_float(o[4 * i])), fabsf(__uint_as_float(o[4 * i + 1]))));
-          mB = fmaxf(mB, fmaxf(fabsf(__uint_as_float(o[4 * i + 2])),
-                               fabsf(__uint_as_float(o[4 * i + 3]))));
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t o[32];
+          tmem_ld16x256b_x8(tO + (uint32_t)(h * 64), o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            mA = fmaxf(mA, fmaxf(fabsf(__uint_as_float(o[4 * i])), fabsf(__uint_as_float(o[4 * i + 1]))));
+            mB = fmaxf(mB, fmaxf(fabsf(__uint_as_float(o[4 * i + 2])),
+                                 fabsf(__uint_as_float(o[4 * i + 3]))));
+          }
         }
         eA = row_exponent(quad_max(mA) * invA);
         eB = row_exponent(quad_max(mB) * invB);
@@ -609,9 +445,14 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
             whole ? pack_bf16x2(x * s, y * s) : pack_f16x2(x * s, y * s);
       };
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        put(rA, i, __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), sA);
-        put(rB, i, __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]), sB);
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t o[32];
+        tmem_ld16x256b_x8(tO + (uint32_t)(h * 64), o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          put(rA, h * 8 + i, __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), sA);
+          put(rB, h * 8 + i, __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]), sB);
+        }
       }
       if (t4 == 0) {
         const float lseA = lrowA > 0.f ? mrefA + __log2f(lrowA) : -INFINITY;
@@ -644,54 +485,260 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       }
       __syncwarp();
     }
-  } else if constexpr (kF8) {
-    // ------------------------------------------------------------ convert
-    // A group of 8 lanes takes two rows, four 16-byte pieces of each; the
-    // rows are paired (r, r ^ 5) at D = 128 and (r, r + 1) at D = 64 so that
-    // both the reads of the 8-bit tile and the writes of the bf16 tile, each
-    // swizzled by its row, touch every bank once.
-    const int cw = warp - L::kWarpMMA - 1;
-    const int oct = lane >> 3, sel = (lane >> 2) & 1, kk = lane & 3;
-    const int sub = D == 128 ? (sel ? oct ^ 5 : oct) : 2 * oct + sel;  // row in its group of 8
-    int tile = 0;
-    bool ok = true;
-    while (ok && walk.next(p, sg)) {
-      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++tile) {
-        const int valid = sg.r.len - t * BN;
-        for (int v = 0; v < 2; ++v) {
-          const int n = 2 * tile + v, rs = n % L::kRawStages, st = tile % L::kStages;
-          uint64_t* empty = v ? &bars->v_empty[st] : &bars->k_empty[st];
-          uint64_t* full = v ? &bars->v_full[st] : &bars->k_full[st];
-          ok = mbar_wait_bounded(&bars->raw_full[rs], (n / L::kRawStages) & 1, abort_flag,
-                                 p.wait_ns);
-          if (ok && tile >= L::kStages)
-            ok = mbar_wait_bounded(empty, (tile / L::kStages - 1) & 1, abort_flag, p.wait_ns);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint8_t* raw = smem + L::kOffRaw + rs * L::kRaw;
-          const uint8_t* sc = smem + L::kOffScale + rs * BN;
-          uint8_t* dst = smem + (v ? L::kOffV : L::kOffK) + st * L::kTile;
-#pragma unroll 2
-          for (int grp = cw; grp < BN / 8; grp += L::kConvWarps) {
-            const int r = grp * 8 + sub;
-            const float f = pow2f((int)sc[r] - 127);
+  } else {
+    if (warp == L::kWarpTMA) {
+      // ------------------------------------------------------------ TMA
+      // Lane l < 16 looks up the page of the tile's 8-key group l, and issues
+      // the copy where that group starts a page (or the tile).
+      int tile = 0;  // tiles issued
+      const int ps = 1 << p.b.page_shift, per = min(ps, BN);
+      if (lane == 0 && work) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+      }
+      bool ok = true;
+      while (ok && next()) {
+        const int32_t* table = p.b.page_table + (int64_t)sg.b * p.b.max_pages;
+        auto look = [&](int t) {
+          const int pos = t * BN + lane * 8;
+          return lane < BN / 8 && t < sg.t1 && pos < sg.r.len
+                     ? __ldg(table + (pos >> p.b.page_shift)) : -1;
+        };
+        int page = look(sg.t0);
+        for (int t = sg.t0; t < sg.t1 && ok; ++t, ++tile) {
+          const int after = look(t + 1);
+          const int pos = t * BN + lane * 8;
+          const bool live = lane < BN / 8 && pos < sg.r.len;
+          int at = page;
+          if (live && (uint32_t)page >= (uint32_t)p.b.num_pages) {
+            atomicOr(p.err, kDevErrBounds);
+            at = p.b.num_pages;  // outside the tensor map: read as zero
+          }
+          const bool lead = live && (lane * 8) % per == 0;
+          const uint32_t bytes =
+              (uint32_t)__popc(__ballot_sync(0xffffffffu, lead)) * per * D * (kF8 ? 1 : 2);
+          const int c1 = pos & (ps - 1) & ~(per - 1), c2 = at * p.b.heads_kv + sg.g;
+          for (int v = 0; v < 2 && ok; ++v) {
+            const CUtensorMap* map = v ? &tmV : &tmK;
+            uint64_t *full, *empty;
+            uint8_t* dst;
+            int round;
+            if constexpr (kF8) {
+              const int n = 2 * tile + v, st = n % L::kRawStages;
+              round = n / L::kRawStages;
+              full = &bars->raw_full[st];
+              empty = &bars->raw_empty[st];
+              dst = smem + L::kOffRaw + st * L::kRaw;
+            } else {
+              const int stages = v ? L::kStagesV : L::kStagesK, st = tile % stages;
+              round = tile / stages;
+              full = v ? &bars->v_full[st] : &bars->k_full[st];
+              empty = v ? &bars->v_empty[st] : &bars->k_empty[st];
+              dst = smem + (v ? L::kOffV : L::kOffK) + st * L::kTile;
+            }
+            if (round > 0)
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait_bounded(empty, (round - 1) & 1, abort_flag, p.wait_ns));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+            __syncwarp();
+            if constexpr (kF8) {
+              if (lead) tma_load_3d(dst + lane * 8 * D, map, full, 0, c1, c2);
+              if (lane < BN / 8) {
+                if (live && at == page) {
+                  const int64_t row = ((int64_t)c2 << p.b.page_shift) + (pos & (ps - 1));
+                  uint8_t* sc = smem + L::kOffScale + ((2 * tile + v) % L::kRawStages) * BN;
+                  cp_async8(sc + lane * 8, (v ? p.v_scale : p.k_scale) + row);
+                }
+                cp_async_arrive(full);
+              }
+            } else if (lead) {
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-              const int c = kk + 4 * half;
-              const uint8_t* src = D == 128 ? raw + r * 128 + ((c ^ sub) << 4) : raw + r * 64 + (c << 4);
-              uint4 lo, hi;
-              expand16(*reinterpret_cast<const uint4*>(src), f, lo, hi);
-              if (r >= valid) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-              uint8_t* d = dst + half * kAtom + r * 128;
-              *reinterpret_cast<uint4*>(d + (((2 * kk) ^ sub) << 4)) = lo;
-              *reinterpret_cast<uint4*>(d + (((2 * kk + 1) ^ sub) << 4)) = hi;
+              for (int a = 0; a < D / 64; ++a)
+                tma_load_3d(dst + a * kAtom + lane * 8 * 128, map, full, a * 64, c1, c2);
+            }
+            __syncwarp();
+          }
+          page = after;
+        }
+      }
+      if (lane == 0) write_split<L::kFixed>(p, share, sg);
+      // copies still in flight must land before the CTA exits (all have, unless
+      // the CTA gave up: then the last tiles' barriers are waited for, those of
+      // copies that were not issued any more running out)
+      if (*abort_flag) {
+        for (int n = max(0, tile - kMaxStages); n <= tile; ++n)
+          for (int v = 0; v < 2; ++v) {
+            const int i = 2 * n + v;
+            uint64_t* full = kF8 ? &bars->raw_full[i % max(1, L::kRawStages)]
+                             : v ? &bars->v_full[n % L::kStagesV] : &bars->k_full[n % L::kStagesK];
+            const int round = kF8 ? i / max(1, L::kRawStages) : n / (v ? L::kStagesV : L::kStagesK);
+            mbar_wait_bounded(full, round & 1, nullptr, kDrainNs / 64);
+          }
+      }
+      __syncwarp();
+    } else if (warp == L::kWarpMMA) {
+      // ------------------------------------------------------------ MMA
+      const bool leader = elect_one_sync();
+      const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(smem + L::kOffK), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(smem + L::kOffV), kAtom, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool r = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns));
+        tc_fence_after();
+        return r;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
+      };
+      int kt = 0, vt = 0;             // K and V tiles consumed
+      int pcnt[2] = {0, 0};           // P tiles consumed per buffer
+      int segs[2] = {0, 0};           // segments per query tile
+      int sbuf = 0, pbuf = 0;         // kQT = 1: the next S / P buffer
+      bool ok = true, first = true;
+      // S of key tile kt for query tile q (all of them share the K stage)
+      auto s_tile = [&](int nq) {
+        const int st = kt % L::kStagesK;
+        if (!wait(&bars->k_full[st], (kt / L::kStagesK) & 1)) return false;
+        for (int q = 0; q < nq; ++q) {
+          const int buf = kQT == 1 ? sbuf : q;
+          if (leader) {
+            issue_s<D>(tmem + buf * BN, desc_at(dQ, q * L::kTile), desc_at(dK, st * L::kTile));
+            tc_commit(&bars->s_full[buf]);
+          }
+          __syncwarp();
+        }
+        sbuf ^= 1;
+        commit(&bars->k_empty[st]);
+        ++kt;
+        return true;
+      };
+      while (ok && next()) {
+        const int n = sg.t1 - sg.t0;
+        if (n == 0) continue;
+        const int rows = sg.r.n * p.G - sg.tp * kQT * BM;
+        const int nq = kQT == 1 ? 1 : min(kQT, cdiv(rows, BM));
+        for (int q = 0; q < nq && ok; ++q) ok = wait(&bars->q_full[q], segs[q] & 1);
+        if (!ok) break;
+        // the first products
+        if (!(ok = s_tile(nq))) break;
+        if (kQT == 1 && n > 1 && !(ok = s_tile(1))) break;
+        if (first && p.stall && !(ok = wait(&bars->never, 0))) break;
+        first = false;
+        for (int j = 0; j < n && ok; ++j) {
+          const int vst = vt % L::kStagesV;
+          if (!(ok = wait(&bars->v_full[vst], (vt / L::kStagesV) & 1))) break;
+          if constexpr (!kF8) {
+            // V rows past the sequence's length: zero, whatever the page holds
+            const int valid = sg.r.len - (sg.t0 + j) * BN;
+            if (valid < BN) {
+              uint8_t* v = smem + L::kOffV + vst * L::kTile;
+              for (int i = lane; i < (BN - valid) * 8; i += 32)
+#pragma unroll
+                for (int a = 0; a < D / 64; ++a)
+                  *reinterpret_cast<uint4*>(v + a * kAtom + valid * 128 + i * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars->raw_empty[rs]);
-            mbar_arrive(full);
+          const uint64_t bv = desc_at(dV, vst * L::kTile);
+          // the next product: tile j + 1 for two query tiles (interleaved with
+          // the P.V products), tile j + 2 for one
+          const bool more = j + (kQT == 1 ? 2 : 1) < n;
+          const int kst = kt % L::kStagesK;
+          for (int q = 0; q < nq; ++q) {
+            const int buf = kQT == 1 ? pbuf : q;
+            if (!(ok = wait(&bars->p_full[buf], pcnt[buf] & 1))) break;
+            ++pcnt[buf];
+            if (leader)
+              issue_pv<D>(tmem + kTmemO + q * D, tmem + buf * BN, bv, j > 0);
+            __syncwarp();
+            if (kQT == 1) {
+              commit(&bars->pv_done);
+            } else if (more) {
+              if (q == 0 && !(ok = wait(&bars->k_full[kst], (kt / L::kStagesK) & 1))) break;
+              if (leader) {
+                issue_s<D>(tmem + q * BN, desc_at(dQ, q * L::kTile), desc_at(dK, kst * L::kTile));
+                tc_commit(&bars->s_full[q]);
+              }
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          pbuf ^= 1;
+          commit(&bars->v_empty[vst]);
+          ++vt;
+          if (more) {
+            if (kQT == 1) {
+              if (!(ok = s_tile(1))) break;
+            } else {
+              commit(&bars->k_empty[kst]);
+              ++kt;
+            }
+          }
+        }
+        if (!ok) break;
+        for (int q = 0; q < nq; ++q) {
+          commit(&bars->o_done[q]);
+          ++segs[q];
+        }
+      }
+      // every MMA issued above has completed before TMEM is released
+      commit(&bars->mma_final);
+      mbar_wait_bounded(&bars->mma_final, 0, nullptr, kDrainNs);
+      __syncwarp();
+    } else if constexpr (kF8) {
+      // ------------------------------------------------------------ convert
+      // A group of 8 lanes takes two rows, four 16-byte pieces of each; the
+      // rows are paired (r, r ^ 5) at D = 128 and (r, r + 1) at D = 64 so that
+      // both the reads of the 8-bit tile and the writes of the bf16 tile, each
+      // swizzled by its row, touch every bank once.
+      const int cw = warp - L::kWarpMMA - 1;
+      const int oct = lane >> 3, sel = (lane >> 2) & 1, kk = lane & 3;
+      const int sub = D == 128 ? (sel ? oct ^ 5 : oct) : 2 * oct + sel;  // row in its group of 8
+      int tile = 0;
+      bool ok = true;
+      while (ok && next()) {
+        for (int t = sg.t0; t < sg.t1 && ok; ++t, ++tile) {
+          const int valid = sg.r.len - t * BN;
+          for (int v = 0; v < 2; ++v) {
+            const int stages = v ? L::kStagesV : L::kStagesK;
+            const int n = 2 * tile + v, rs = n % L::kRawStages, st = tile % stages;
+            uint64_t* empty = v ? &bars->v_empty[st] : &bars->k_empty[st];
+            uint64_t* full = v ? &bars->v_full[st] : &bars->k_full[st];
+            ok = mbar_wait_bounded(&bars->raw_full[rs], (n / L::kRawStages) & 1, abort_flag,
+                                   p.wait_ns);
+            if (ok && tile >= stages)
+              ok = mbar_wait_bounded(empty, (tile / stages - 1) & 1, abort_flag, p.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t* raw = smem + L::kOffRaw + rs * L::kRaw;
+            const uint8_t* sc = smem + L::kOffScale + rs * BN;
+            uint8_t* dst = smem + (v ? L::kOffV : L::kOffK) + st * L::kTile;
+#pragma unroll 2
+            for (int grp = cw; grp < BN / 8; grp += L::kConvWarps) {
+              const int r = grp * 8 + sub;
+              const float f = pow2f((int)sc[r] - 127);
+#pragma unroll
+              for (int half = 0; half < D / 64; ++half) {
+                const int c = kk + 4 * half;
+                const uint8_t* src = D == 128 ? raw + r * 128 + ((c ^ sub) << 4) : raw + r * 64 + (c << 4);
+                uint4 lo, hi;
+                expand16(*reinterpret_cast<const uint4*>(src), f, lo, hi);
+                if (r >= valid) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                uint8_t* d = dst + half * kAtom + r * 128;
+                *reinterpret_cast<uint4*>(d + (((2 * kk) ^ sub) << 4)) = lo;
+                *reinterpret_cast<uint4*>(d + (((2 * kk + 1) ^ sub) << 4)) = hi;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bars->raw_empty[rs]);
+              mbar_arrive(full);
+            }
           }
         }
       }
