@@ -62,7 +62,6 @@ using namespace paged;
 constexpr int BM = 128;  // query rows per tile
 constexpr uint32_t kAtom = 128 * 128;  // 128 rows of one 128-byte swizzle atom (64 bf16)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 2 * BN;    // S buffers first
 constexpr float kLazy = 8.0f;          // log2 units
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMaxStages = 6, kMaxRaw = 8;
@@ -71,8 +70,8 @@ struct Barriers {
   uint64_t q_full[2];
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
-  uint64_t s_full[2], p_full[2], o_done[2];
-  uint64_t pv_done, mma_final;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t mma_final;
   uint64_t never;  // completed by nothing: the target of the test stall
   uint32_t tmem_base;
   int abort;
@@ -98,6 +97,14 @@ struct Lay {
   static constexpr uint32_t kOffScale = kOffRaw + kRawStages * kRaw;
   static constexpr uint32_t kOffBar = kOffScale + kRawStages * BN;
   static constexpr uint32_t kSmem = kOffBar + sizeof(Barriers) + 1024;
+  // Tensor memory: S buffers, then (two query tiles) P, then O.  With two query
+  // tiles P has columns of its own, so that a score buffer is free again as
+  // soon as the softmax has loaded it; at D = 128 that leaves one for both.
+  static constexpr bool kSep = kQT == 2 && !kF8;
+  static constexpr int kSBufs = kSep && D == 128 ? 1 : 2;
+  static constexpr uint32_t kTmemP = kSBufs * BN;
+  static constexpr uint32_t kTmemO = kTmemP + (kSep ? kQT * BN / 2 : 0);
+  static_assert(kTmemO + kQT * D <= kTmemCols, "tensor memory");
   // an item's overhead (its Q tile, first product and epilogue) in key tiles
   static constexpr int kFixed = kQT == 1 ? 2 : 3;
   static constexpr int kMinShare = kFixed;
@@ -176,10 +183,10 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(&bars->q_full[q], 8);
       mbar_init(&bars->s_full[q], 1);
+      mbar_init(&bars->s_free[q], 8);
       mbar_init(&bars->p_full[q], 8);
-      mbar_init(&bars->o_done[q], 1);
+      mbar_init(&bars->pv_done[q], 1);
     }
-    mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->mma_final, 1);
     mbar_init(&bars->never, 1);
     bars->abort = 0;
@@ -222,11 +229,11 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
     const int rbase = wl * 32 + hv * 16;
     const int rA = rbase + (lane >> 2), rB = rA + 8;  // query rows in tile q
     const uint32_t lane_base = (uint32_t)rbase << 16;
-    const uint32_t tO = tmem + lane_base + kTmemO + (uint32_t)(q * D);
+    const uint32_t tO = tmem + lane_base + L::kTmemO + (uint32_t)(q * D);
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     constexpr int kChunks = D / 8;  // 16-byte pieces of a row
     uint8_t* tileQ = smem + q * L::kTile;
-    int cnt = 0, seg = 0;  // tiles and segments of this query tile
+    int cnt = 0;  // tiles of this query tile
     bool ok = true;
     auto quad_max = [](float v) {
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -235,6 +242,13 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
     auto quad_sum = [](float v) {
       v += __shfl_xor_sync(0xffffffffu, v, 1);
       return v + __shfl_xor_sync(0xffffffffu, v, 2);
+    };
+    // P.V product t of this query tile is complete
+    auto wait_pv = [&](int t) {
+      const bool done = __all_sync(
+          0xffffffffu, mbar_wait_bounded(&bars->pv_done[q], t & 1, abort_flag, p.wait_ns));
+      tc_fence_after();
+      return done;
     };
     while (ok && next()) {
       const int row0 = (sg.tp * kQT + q) * BM;         // packed row of the tile's row 0
@@ -294,7 +308,8 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       for (int j = 0; j < n; ++j, ++cnt) {
         const int buf = kQT == 1 ? cnt & 1 : q;
         const uint32_t par = (kQT == 1 ? cnt >> 1 : cnt) & 1;
-        const uint32_t tS = tmem + lane_base + (uint32_t)(buf * BN);
+        const uint32_t tS = tmem + lane_base + (uint32_t)((L::kSBufs == 1 ? 0 : buf) * BN);
+        const uint32_t tP = L::kSep ? tmem + lane_base + L::kTmemP + (uint32_t)(q * (BN / 2)) : tS;
         // wait outcomes are made warp-uniform: tcgen05.ld/st are .sync.aligned
         if (!__all_sync(0xffffffffu,
                         mbar_wait_bounded(&bars->s_full[buf], par, abort_flag, p.wait_ns))) {
@@ -325,10 +340,16 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
               }
             }
           };
+          auto free_s = [&]() {  // the score buffer may be written again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->s_free[q]);
+          };
           float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
           for (int h = kH - 1; h >= 0; --h) {
             load(h);
+            if (L::kSep && kH == 1) free_s();
 #pragma unroll
             for (int i = 0; i < kI; ++i) {
               ma = fmaxf(ma, fmaxf(__uint_as_float(sv[4 * i]), __uint_as_float(sv[4 * i + 1])));
@@ -343,14 +364,12 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
             mrefB = fmaxf(mrefB, xb);
           } else if (__any_sync(0xffffffffu, xa > mrefA + kLazy || xb > mrefB + kLazy)) {
             // rescale (rare, a warp-uniform decision); the last P.V product
-            // has to be complete
-            if (kQT == 1 &&
-                !__all_sync(0xffffffffu, mbar_wait_bounded(&bars->pv_done, (cnt - 1) & 1,
-                                                           abort_flag, p.wait_ns))) {
+            // has to be complete (where P lies in the place of S, and there
+            // are two query tiles, it is: S came behind it)
+            if ((kQT == 1 || L::kSep) && !wait_pv(cnt - 1)) {
               ok = false;
               break;
             }
-            if (kQT == 1) tc_fence_after();
             const float na = fmaxf(mrefA, xa), nb = fmaxf(mrefB, xb);
             const float alA = ex2_approx(mrefA - na), alB = ex2_approx(mrefB - nb);
             lA *= alA;
@@ -367,11 +386,19 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
             mrefA = na;
             mrefB = nb;
           }
+          // P has columns of its own: the last P.V product has to have read them
+          if (L::kSep && cnt > 0 && !wait_pv(cnt - 1)) {
+            ok = false;
+            break;
+          }
           const float2 na = make_float2(-mrefA, -mrefA), nb = make_float2(-mrefB, -mrefB);
           float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            if (h > 0) load(h);
+            if (h > 0) {
+              load(h);
+              if (L::kSep) free_s();
+            }
             uint32_t w[2 * kI];  // 16x128b: w[2i] row A, w[2i + 1] row B, column 4 i + t % 4
 #pragma unroll
             for (int i = 0; i < kI; ++i) {
@@ -387,25 +414,32 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
               w[2 * i] = pack_bf16x2(pa.x, pa.y);
               w[2 * i + 1] = pack_bf16x2(pb.x, pb.y);
             }
-            if constexpr (kH == 1) tmem_st16x128b_x16(tS, w);
-            else tmem_st16x128b_x8(tS + (uint32_t)(h * 32), w);
+            if constexpr (kH == 1) tmem_st16x128b_x16(tP, w);
+            else tmem_st16x128b_x8(tP + (uint32_t)(h * 32), w);
           }
           lA += sa.x + sa.y;
           lB += sb.x + sb.y;
           tmem_wait_st();
           tc_fence_before();
+        } else if (L::kSep) {
+          // (an arrival must not run ahead of the other warps' previous one)
+          if (lane == 0) mbar_arrive(&bars->s_free[q]);
+          if (cnt > 0 && !wait_pv(cnt - 1)) {
+            ok = false;
+            break;
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[buf]);
       }
       if (!ok) break;
       // epilogue: O / l and the log-sum-exp
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait_bounded(&bars->o_done[q], seg & 1, abort_flag, p.wait_ns))) {
+      // (a wait tells a phase from the one before it only, so the last but one
+      // comes first where nothing else has waited for it)
+      if (((kQT == 1 || L::kSep) && cnt > 1 && !wait_pv(cnt - 2)) || !wait_pv(cnt - 1)) {
         ok = false;
         break;
       }
-      ++seg;
       if (!active) continue;
       tc_fence_after();
       const float lrowA = quad_sum(lA), lrowB = quad_sum(lB);
@@ -592,41 +626,58 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
         if (leader) tc_commit(bar);
         __syncwarp();
       };
-      int kt = 0, vt = 0;             // K and V tiles consumed
-      int pcnt[2] = {0, 0};           // P tiles consumed per buffer
-      int segs[2] = {0, 0};           // segments per query tile
-      int sbuf = 0, pbuf = 0;         // kQT = 1: the next S / P buffer
+      int kt = 0, vt = 0;            // K and V tiles consumed
+      int cnt[2] = {0, 0};           // tiles of the query tiles (kQT = 1: of the S buffers)
+      int segs[2] = {0, 0};          // segments per query tile
+      int sbuf = 0, pbuf = 0;        // kQT = 1: the next S / P buffer
       bool ok = true, first = true;
-      // S of key tile kt for query tile q (all of them share the K stage)
-      auto s_tile = [&](int nq) {
-        const int st = kt % L::kStagesK;
-        if (!wait(&bars->k_full[st], (kt / L::kStagesK) & 1)) return false;
-        for (int q = 0; q < nq; ++q) {
-          const int buf = kQT == 1 ? sbuf : q;
-          if (leader) {
-            issue_s<D>(tmem + buf * BN, desc_at(dQ, q * L::kTile), desc_at(dK, st * L::kTile));
-            tc_commit(&bars->s_full[buf]);
-          }
-          __syncwarp();
+      auto wait_k = [&](int t) { return wait(&bars->k_full[t % L::kStagesK], (t / L::kStagesK) & 1); };
+      auto s_product = [&](int q, int buf, int t, uint64_t* full) {
+        if (leader) {
+          issue_s<D>(tmem + buf * BN, desc_at(dQ, q * L::kTile),
+                     desc_at(dK, t % L::kStagesK * L::kTile));
+          tc_commit(full);
         }
-        sbuf ^= 1;
-        commit(&bars->k_empty[st]);
-        ++kt;
-        return true;
+        __syncwarp();
       };
       while (ok && next()) {
         const int n = sg.t1 - sg.t0;
         if (n == 0) continue;
         const int rows = sg.r.n * p.G - sg.tp * kQT * BM;
         const int nq = kQT == 1 ? 1 : min(kQT, cdiv(rows, BM));
-        for (int q = 0; q < nq && ok; ++q) ok = wait(&bars->q_full[q], segs[q] & 1);
-        if (!ok) break;
-        // the first products
-        if (!(ok = s_tile(nq))) break;
-        if (kQT == 1 && n > 1 && !(ok = s_tile(1))) break;
-        if (first && p.stall && !(ok = wait(&bars->never, 0))) break;
+        for (int q = 0; q < nq && ok; ++q) ok = wait(&bars->q_full[q], segs[q]++ & 1);
+        // S of the segment's tile j for query tile q.  A shared S buffer is
+        // waited for until the other query tile has loaded it, an own one
+        // until this one has (one query tile: P has taken its place, and the
+        // P.V product issued before has read it).
+        auto s_of = [&](int q, int j) {
+          const int t = kt + j;
+          if (q == 0 && !wait_k(t)) return false;
+          if constexpr (kQT == 1) {
+            s_product(0, sbuf, t, &bars->s_full[sbuf]);
+            sbuf ^= 1;
+          } else {
+            constexpr bool kOne = L::kSBufs == 1;
+            if (L::kSep) {
+              // tile j of q = 0 comes after tile j - 1 of q = 1, tile j of
+              // q = 1 after tile j of q = 0
+              const int o = kOne && nq == 2 ? 1 - q : q;
+              const int past = kOne && nq == 2 && q == 1 ? j : j - 1;
+              if (past >= 0 && !wait(&bars->s_free[o], (cnt[o] + past) & 1)) return false;
+            }
+            s_product(q, kOne ? 0 : q, t, &bars->s_full[q]);
+          }
+          if (q == nq - 1) commit(&bars->k_empty[t % L::kStagesK]);
+          return true;
+        };
+        ok = ok && s_of(0, 0);
+        if (kQT == 1) ok = ok && (n == 1 || s_of(0, 1));
+        else ok = ok && (nq == 1 || s_of(1, 0));
+        if (ok && first && p.stall) ok = wait(&bars->never, 0);
         first = false;
         for (int j = 0; j < n && ok; ++j) {
+          // separate P: the next S of a query tile goes ahead of its P.V
+          if (L::kSep && j + 1 < n && !(ok = s_of(0, j + 1))) break;
           const int vst = vt % L::kStagesV;
           if (!(ok = wait(&bars->v_full[vst], (vt / L::kStagesV) & 1))) break;
           if constexpr (!kF8) {
@@ -644,46 +695,28 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
             }
           }
           const uint64_t bv = desc_at(dV, vst * L::kTile);
-          // the next product: tile j + 1 for two query tiles (interleaved with
-          // the P.V products), tile j + 2 for one
-          const bool more = j + (kQT == 1 ? 2 : 1) < n;
-          const int kst = kt % L::kStagesK;
-          for (int q = 0; q < nq; ++q) {
+          for (int q = 0; q < nq && ok; ++q) {
+            if (L::kSep && q == 1 && j + 1 < n && !(ok = s_of(1, j + 1))) break;
             const int buf = kQT == 1 ? pbuf : q;
-            if (!(ok = wait(&bars->p_full[buf], pcnt[buf] & 1))) break;
-            ++pcnt[buf];
-            if (leader)
-              issue_pv<D>(tmem + kTmemO + q * D, tmem + buf * BN, bv, j > 0);
+            const uint32_t par = kQT == 1 ? cnt[buf]++ : cnt[q] + j;
+            if (!(ok = wait(&bars->p_full[buf], par & 1))) break;
+            const uint32_t aP = L::kSep ? L::kTmemP + q * (BN / 2) : buf * BN;
+            if (leader) issue_pv<D>(tmem + L::kTmemO + q * D, tmem + aP, bv, j > 0);
             __syncwarp();
-            if (kQT == 1) {
-              commit(&bars->pv_done);
-            } else if (more) {
-              if (q == 0 && !(ok = wait(&bars->k_full[kst], (kt / L::kStagesK) & 1))) break;
-              if (leader) {
-                issue_s<D>(tmem + q * BN, desc_at(dQ, q * L::kTile), desc_at(dK, kst * L::kTile));
-                tc_commit(&bars->s_full[q]);
-              }
-              __syncwarp();
-            }
+            commit(&bars->pv_done[q]);
+            // P in the place of S: the next S has to come behind its P.V
+            if (!L::kSep && kQT == 2 && j + 1 < n) ok = s_of(q, j + 1);
           }
           if (!ok) break;
           pbuf ^= 1;
           commit(&bars->v_empty[vst]);
           ++vt;
-          if (more) {
-            if (kQT == 1) {
-              if (!(ok = s_tile(1))) break;
-            } else {
-              commit(&bars->k_empty[kst]);
-              ++kt;
-            }
-          }
+          if (kQT == 1 && j + 2 < n) ok = s_of(0, j + 2);
         }
         if (!ok) break;
-        for (int q = 0; q < nq; ++q) {
-          commit(&bars->o_done[q]);
-          ++segs[q];
-        }
+        kt += n;
+        if (kQT == 2)
+          for (int q = 0; q < nq; ++q) cnt[q] += n;
       }
       // every MMA issued above has completed before TMEM is released
       commit(&bars->mma_final);
