@@ -100,7 +100,9 @@ struct Lay {
   // Tensor memory: S buffers, then (two query tiles) P, then O.  With two query
   // tiles P has columns of its own, so that a score buffer is free again as
   // soon as the softmax has loaded it; at D = 128 that leaves one for both.
-  static constexpr bool kSep = kQT == 2 && !kF8;
+  // (With an 8-bit cache the softmax loads its scores twice, and holds a single
+  // buffer too long: ragged blocks of 8 took 176 us against 137.)
+  static constexpr bool kSep = kQT == 2 && (!kF8 || D == 64);
   static constexpr int kSBufs = kSep && D == 128 ? 1 : 2;
   static constexpr uint32_t kTmemP = kSBufs * BN;
   static constexpr uint32_t kTmemO = kTmemP + (kSep ? kQT * BN / 2 : 0);
