@@ -698,6 +698,12 @@ class _on:
             self._guard.__exit__(*exc)
 
 
+def _own(workspace: torch.Tensor, device):
+    if workspace.device != device or workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected "
+                         f"torch.uint8 on {device}")
+
+
 def _lent(t: torch.Tensor, stream) -> torch.Tensor:
     """A tensor allocated here, on the current stream, for a call on `stream`:
     its memory is not reused before that stream is done with it."""
@@ -809,6 +815,7 @@ def cache_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     with _on(dev, stream) as st:
         if workspace is None:
             workspace = _lent(new_workspace(int(lib.dd_cache_workspace()), dev, stream), stream)
+        _own(workspace, dev)
         _check(lib.dd_cache_append(cache._ref, batch._c(k_new.shape[0]), k_new.data_ptr(), ks,
                                    v_new.data_ptr(), vs, workspace.data_ptr(), workspace.numel(),
                                    st))
@@ -837,6 +844,7 @@ def cache_read(cache: PagedCache, page_table: torch.Tensor, cu_prefix: torch.Ten
     with _on(dev, stream) as st:
         if workspace is None:
             workspace = _lent(new_workspace(int(lib.dd_cache_workspace()), dev, stream), stream)
+        _own(workspace, dev)
         _check(lib.dd_cache_read(cache._ref, B, pages, page_table.data_ptr(),
                                  cu_prefix.data_ptr(), total, k_out.data_ptr(), v_out.data_ptr(),
                                  workspace.data_ptr(), workspace.numel(), st))
@@ -871,6 +879,7 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, batch: PagedBatch,
         if workspace is None:
             workspace = _lent(new_workspace(paged_attn_workspace_bytes(cache, batch, T, Hq), dev,
                                             stream), stream)
+        _own(workspace, dev)
         _check(lib.dd_paged_attn(cache._ref, batch._c(T), Hq, q.data_ptr(), qs,
                                  float(scale if scale is not None else D ** -0.5), int(causal),
                                  out.data_ptr(), None if lse is None else lse.data_ptr(),
@@ -930,6 +939,7 @@ def verify_draft(target_logits: torch.Tensor, draft_logits: torch.Tensor,
             workspace = _lent(new_workspace(verify_draft_workspace_bytes(B, T, V), dev, stream),
                               stream)
         prm = VerifyParams(float(temperature), float(draft_temperature))
+        _own(workspace, dev)
         _check(lib.dd_verify_draft(
             ctypes.byref(prm), _dtype_code(target_logits), B, T, V, target_logits.data_ptr(),
             zt[0] if T + B > 1 else V, draft_logits.data_ptr(),

@@ -1120,8 +1120,8 @@ dd_status check_paged_batch(const dd_paged_cache* c, const dd_paged_batch* b, bo
   if (b->batch < 0 || b->total_new < 0 || b->max_new < 0 || b->max_pages < 1)
     return fail(DD_ERR_INVALID_ARG, "batch=%d total_new=%d max_new=%d max_pages=%d", b->batch,
                 b->total_new, b->max_new, b->max_pages);
-  if ((int64_t)b->max_pages * c->page_size > INT32_MAX)
-    return fail(DD_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^31");
+  if ((int64_t)b->max_pages * c->page_size > (1 << 30))
+    return fail(DD_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^30");
   if (!pointers || b->batch == 0) return DD_OK;
   if (!b->page_table || !b->cu_new || !b->kv_len)
     return fail(DD_ERR_INVALID_ARG, "NULL page_table, cu_new or kv_len");

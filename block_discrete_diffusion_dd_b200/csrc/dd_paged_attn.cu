@@ -49,7 +49,6 @@
 // Every mbarrier wait is bounded in time; on expiry the CTA latches an error,
 // drains its copies and MMAs and frees its tensor memory.
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "dd_paged_attn.cuh"
@@ -835,14 +834,9 @@ template <int D, bool kF8, int kQT>
 cudaError_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, int sms,
                      cudaStream_t stream) {
   using L = Lay<D, kF8, kQT>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(paged_attn_kernel<D, kF8, kQT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
-  });
-  if (attr != cudaSuccess) return attr;
-  cudaError_t e = launch_pdl(paged_attn_kernel<D, kF8, kQT>, dim3(sms), dim3(L::kThreads), L::kSmem,
+  cudaError_t e = allow_smem<paged_attn_kernel<D, kF8, kQT>>((int)L::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_kernel<D, kF8, kQT>, dim3(sms), dim3(L::kThreads), L::kSmem,
                              stream, mk, mv, p);
   note_launch();
   return e;

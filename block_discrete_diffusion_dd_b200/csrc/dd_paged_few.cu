@@ -33,8 +33,6 @@
 // that of 2^(x - m) = w 2^-ev.  The bf16 query is scaled by a power of two per
 // row that puts its largest magnitude in [2^14, 2^15); only what lies 2^28
 // below it loses bits.
-#include <mutex>
-
 #include "dd_paged_attn.cuh"
 
 namespace dd {
@@ -448,14 +446,9 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
 template <int D, bool kF8, int NT>
 cudaError_t launch_t(const Params& p, const PagedPool& pool, int sms, cudaStream_t stream) {
   using F = Few<D, kF8, NT>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(paged_few_kernel<D, kF8, NT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
-  });
-  if (attr != cudaSuccess) return attr;
-  cudaError_t e = launch_pdl(paged_few_kernel<D, kF8, NT>, dim3(F::kBlocks * sms),
+  cudaError_t e = allow_smem<paged_few_kernel<D, kF8, NT>>(F::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_few_kernel<D, kF8, NT>, dim3(F::kBlocks * sms),
                              dim3(F::kThreads), F::kSmem, stream, p,
                              static_cast<const uint8_t*>(pool.k),
                              static_cast<const uint8_t*>(pool.v));

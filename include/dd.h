@@ -504,9 +504,11 @@ DD_API dd_status dd_denoise_block_adaptive_graph_destroy(dd_adaptive_graph graph
  * length up to its bounds, and the host is never waited for.  What they hold
  * is checked on the device: a batch row with impossible values (see
  * dd_paged_batch) is taken as empty, a page id outside the pool is never
- * followed, and both latch DD_ERR_DEVICE_BOUNDS in the workspace.  Their
- * workspaces need no state between calls beyond the error word, so calls of
- * any shape may share one, as long as they do not overlap in time. */
+ * followed, and both latch DD_ERR_DEVICE_BOUNDS in the workspace.  Besides
+ * the error word their workspaces hold 4 KB of counters, which every
+ * completed call leaves cleared and dd_verify_draft does not touch: calls of
+ * this family, of any shape, may share a workspace (cleared once with
+ * dd_workspace_init) as long as they do not overlap in time. */
 
 /* A cache of pages.  One page holds page_size consecutive positions of one
  * sequence, for every kv head.
@@ -528,7 +530,7 @@ typedef struct {
 
 /* A batch of sequences with new tokens, packed one after the other.
  *   batch       B >= 0 sequences
- *   max_pages   entries per row of page_table; max_pages * page_size < 2^31
+ *   max_pages   entries per row of page_table; max_pages * page_size <= 2^30
  *   total_new   rows of the packed new-token tensors; rows at or past
  *               cu_new[B] belong to no sequence, are not read, and their
  *               outputs are left as they were

@@ -349,3 +349,155 @@ def test_paged_attention_equals_canvas_attention_on_the_packed_cache():
                            kp[:700], vp[:700], pre.to(DEV), pre)
     diff = (o2[0].double() - out.double()).abs().max().item()
     assert diff <= 2.0 ** -6
+
+
+def test_attention_wide_batch_with_long_chunks():
+    # more sequences than the tensor-core kernel has threads, a few of them long
+    g = torch.Generator().manual_seed(2)
+    new = torch.randint(0, 2, (1000,), generator=g).tolist()
+    past = torch.randint(0, 30, (1000,), generator=g).tolist()
+    new[7], new[640], new[999] = 150, 20, 33
+    pr = ref.problem(new, past, 8)
+    cache, k64, v64 = _pool(pr, 1, 64, "bf16")
+    _check_attn(_normal((sum(new), 2, 64), 14), cache, k64, v64, pr)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,G,D,new,past", [
+    (2, 2, 128, (3, 2, 1, 0), (-1, -2, 0, 5)),  # few rows, some of which see nothing
+    (1, 100, 64, (1, 3), (700, 5)),             # one kv head for a hundred query heads
+    (1, 128, 128, (2,), (300,)),
+    (2, 5, 128, (60, 1), (0, 2000)),            # one query tile, odd group
+])
+def test_attention_row_counts(kind, H, G, D, new, past):
+    pr = ref.problem(new, past, 16, seed=G)
+    cache, k64, v64 = _pool(pr, H, D, kind, seed=G)
+    _check_attn(_normal((sum(new), H * G, D), 15), cache, k64, v64, pr)
+
+
+def test_pool_beyond_32_bit_offsets():
+    # pages whose first byte lies past 2^32: 8 heads of 64 x 128 bf16 take
+    # 128 KB a page
+    H, D, ps, pages = 8, 128, 64, 33000
+    cache = dd.new_paged_cache(pages, ps, H, D)
+    new, past = (70, 1), (0, 0)
+    table = torch.tensor([[pages - 1, 32768], [32900, 0]], dtype=torch.int32)
+    x = _normal((71, 3 * H, D), 16)
+    dev = x.to(DEV)
+    cu = torch.tensor([0, 70, 71], dtype=torch.int32)
+    lens = torch.tensor([70, 1], dtype=torch.int32)
+    batch = dd.PagedBatch(table.to(DEV), cu.to(DEV), lens.to(DEV), 70)
+    ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, 71, H))
+    dd.cache_append(cache, batch, dev[:, H:2 * H], dev[:, 2 * H:], workspace=ws)
+    out, lse = dd.paged_attn(dev[:, :H], cache, batch, want_lse=True, workspace=ws)
+    kp, vp = dd.cache_read(cache, batch.page_table, batch.cu_new, total=71, workspace=ws)
+    dd.query_device_error(ws)
+    assert torch.equal(kp.cpu(), x[:, H:2 * H]) and torch.equal(vp.cpu(), x[:, 2 * H:])
+    one, _ = dd.paged_attn(dev[70:, :H], cache, dd.PagedBatch(
+        batch.page_table[1:], torch.tensor([0, 1], dtype=torch.int32, device=DEV),
+        batch.kv_len[1:], 1))
+    assert torch.equal(one[0].cpu(), x[70, 2 * H:])  # a single key: its value
+    pr = ref.Problem(ps, torch.tensor([[1, 0], [2, 0]]), cu, lens, 3, list(new), [70, 1])
+    pool = torch.zeros((2, 3, H, ps, D), dtype=torch.float64)
+    for i in range(70):
+        pool[:, 1 if i < 64 else 0, :, i % 64] = torch.stack([x[i, H:2 * H], x[i, 2 * H:]]).double()
+    pool[:, 2, :, 0] = torch.stack([x[70, H:2 * H], x[70, 2 * H:]]).double()
+    want, wlse, mag = ref.attention(x[:, :H], pool[0], pool[1], pr, D ** -0.5, True)
+    err = (out.double().cpu() - want).abs()
+    tol = (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * mag +
+           2.0 ** -11 * want.abs().amax(-1, keepdim=True))
+    assert (err <= tol).all()
+    assert (lse.double().cpu() - wlse).abs().max() <= 1e-4
+
+
+def test_two_calls_at_once_on_their_own_streams():
+    # long enough to overlap, one with few rows and one with many
+    cases = []
+    for new, past, kind in (((1,) * 8, (6000,) * 8, "e4m3"), ((200, 256), (4000, 3000), "bf16")):
+        pr = ref.problem(new, past, 16, seed=len(new))
+        H, D = 4, 128
+        k, v = (torch.randn((pr.pages, H, 16, D), device=DEV).to(torch.bfloat16) for _ in range(2))
+        cache = dd.PagedCache(k, v)
+        if kind == "e4m3":
+            s = torch.full((pr.pages, H, 16), 120, dtype=torch.uint8, device=DEV)
+            cache = dd.PagedCache(k.to(E4M3), v.to(E4M3), s, s.clone())
+        q = torch.randn((sum(new), 8, D), device=DEV).to(torch.bfloat16)
+        batch = _batch(pr)
+        ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, q.shape[0], 8))
+        want, _ = dd.paged_attn(q, cache, batch, workspace=ws)
+        cases.append((q, cache, batch, ws, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[] for _ in cases]
+    for _ in range(5):
+        for i, (q, cache, batch, ws, _) in enumerate(cases):
+            outs[i].append(dd.paged_attn(q, cache, batch, workspace=ws, stream=streams[i])[0])
+    torch.cuda.synchronize()
+    for i, (_, _, _, ws, want) in enumerate(cases):
+        dd.query_device_error(ws)
+        assert all(torch.equal(o, want) for o in outs[i])
+
+
+def test_captured_calls_that_share_a_workspace():
+    # two graphs (few rows, many rows) replayed in turn on one workspace, with
+    # calls of the other operators of the family between them
+    pr1 = ref.problem((1,) * 5, (900, 40, 3000, 7, 128), 16, seed=1)
+    pr2 = ref.problem((70, 130), (500, 1500), 16, seed=2)
+    work = []
+    for pr in (pr1, pr2):
+        cache, _, _ = _pool(pr, 2, 64, "bf16")
+        q = _normal((sum(pr.new), 4, 64), 17).to(DEV)
+        work.append((q, cache, _batch(pr), torch.empty_like(q)))
+    V = 1000
+    logits = torch.randn((9, V), device=DEV)
+    draft = [torch.randn((7, V), device=DEV), torch.zeros(7, dtype=torch.int32, device=DEV),
+             torch.full((7,), 0.5, device=DEV),
+             torch.tensor([0, 3, 7], dtype=torch.int32, device=DEV),
+             torch.full((7,), 0.999, device=DEV), torch.tensor([0.2, 0.8], device=DEV)]
+    n = max([dd.paged_attn_workspace_bytes(c, b, q.shape[0], 4) for q, c, b, _ in work] +
+            [dd.verify_draft_workspace_bytes(2, 7, V)])
+    ws = dd.new_workspace(n)
+    graphs, want = [], []
+    for q, cache, batch, out in work:
+        dd.paged_attn(q, cache, batch, out=out, workspace=ws)
+        want.append(out.clone())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                dd.paged_attn(q, cache, batch, out=out, workspace=ws)
+        torch.cuda.current_stream().wait_stream(side)
+        graphs.append(graph)
+    first = None
+    for _ in range(3):
+        for i, graph in enumerate(graphs):
+            work[i][3].zero_()
+            graph.replay()
+            assert torch.equal(work[i][3], want[i])
+            o = dd.verify_draft(logits, *draft, workspace=ws)
+            first = first or {k: t.clone() for k, t in o.items()}
+            assert all(torch.equal(o[k], first[k]) for k in o)
+    dd.query_device_error(ws)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [20, 200])
+def test_timeout_is_reported_and_the_next_call_is_right(kind, new):
+    # the tensor-core kernel stalls on a barrier that nothing completes, gives
+    # up after 100 us and frees what it holds
+    pr = ref.problem((new, 3), (700, 90), 16)
+    cache, k64, v64 = _pool(pr, 2, 128, kind)
+    q = _normal((new + 3, 4, 128), 18)
+    batch = _batch(pr)
+    ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, new + 3, 4))
+    dd.set_test_stall_ns(100_000)
+    try:
+        dd.paged_attn(q.to(DEV), cache, batch, workspace=ws)
+        with pytest.raises(dd.DDError) as err:
+            dd.query_device_error(ws)
+    finally:
+        dd.set_test_stall_ns(0)
+    assert err.value.status == 5  # DD_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        _check_attn(q, cache, k64, v64, pr)

@@ -171,3 +171,31 @@ def test_verify_follows_the_target_distribution():
     p = torch.softmax(zt.double(), 0)
     n = torch.bincount(o["tokens"][0::2].long(), minlength=V).double()
     assert ((n - B * p).abs() <= 5 * (B * p * (1 - p)).sqrt()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_verify_decides_near_ties_in_64_bits(dtype):
+    # u conf within a few fp32 steps of p on either side, row after row: far
+    # closer than the fp32 sums of the scan can tell
+    k, V = (40, 40), 5000
+    c, tau, tau_d = _case(k, V, dtype, 21, noise=0.3)
+    p = torch.cat([torch.softmax(c["target_logits"][b * 41:b * 41 + 40].double(), -1)
+                   for b in range(2)])
+    p = p.gather(1, c["draft_tokens"][:, None].long())[:, 0]
+    c["draft_conf"] = (p * 2).float()
+    u = (p / c["draft_conf"].double()).float()
+    steps = torch.arange(80) % 5 - 4  # -4 .. 0 steps of u: the last ones around the border
+    bits = u.view(torch.int32) + steps.to(torch.int32)
+    c["u_accept"] = bits.view(torch.float32)
+    _check(c, tau, tau_d)
+
+
+def test_verify_on_another_stream():
+    c, tau, tau_d = _case((5, 9), 20000, torch.bfloat16, 22)
+    want = _run(c, tau, tau_d)
+    dev = {k: v.to(DEV) for k, v in c.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o = dd.verify_draft(**dev, temperature=tau, draft_temperature=tau_d, stream=side)
+    side.synchronize()
+    assert all(torch.equal(o[x].cpu(), want[x]) for x in want)
