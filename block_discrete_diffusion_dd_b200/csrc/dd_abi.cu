@@ -1182,8 +1182,9 @@ dd_status check_heads_q(int heads_q, int heads_kv) {
 
 }  // namespace
 
-// Behind the header, the workspaces of this family keep the counters of the
-// attention's merge, so that its calls may share one with the others.
+// Behind the header, the workspaces of this family keep counters (of the
+// attention's merge, of the verification's rows) that every call leaves
+// cleared, so that calls of any of them may share one.
 static constexpr size_t kPagedHeader = kHeaderBytes + kPagedCounters * sizeof(uint32_t);
 
 size_t dd_cache_workspace(void) { return kHeaderBytes; }
@@ -1353,6 +1354,7 @@ dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int ba
   a.tokens = tokens;
   a.target_prob = target_prob;
   a.err = static_cast<uint32_t*>(workspace);
+  a.arrived = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
   a.scratch = static_cast<uint8_t*>(workspace) + kPagedHeader;
   cudaError_t e = launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "draft verification");

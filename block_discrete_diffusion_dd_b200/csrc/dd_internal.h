@@ -218,6 +218,10 @@ struct CacheReadArgs {
 };
 cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t stream);
 
+// Counters in a workspace that are zero before the first call and after every
+// call; at least twice the SMs.
+constexpr size_t kPagedCounters = 1024;
+
 // Attention of a chunk of new tokens over the paged cache (dd_paged_attn.cu).
 struct PagedAttnArgs {
   PagedBatch p;
@@ -230,10 +234,9 @@ struct PagedAttnArgs {
   void* out;   // bf16 [total_new, heads_q, head_dim]
   float* lse;  // fp32 [total_new, heads_q] or NULL
   uint32_t* err;
-  uint32_t* arrived;  // kPagedCounters, zero before the first call and after every call
+  uint32_t* arrived;  // kPagedCounters
   void* scratch;      // paged_attn_scratch_bytes
 };
-constexpr size_t kPagedCounters = 1024;  // at least twice the SMs
 size_t paged_attn_scratch_bytes(const PagedAttnArgs& a);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 
@@ -251,7 +254,8 @@ struct VerifyArgs {
   int32_t *accepted, *tokens;
   float* target_prob;
   uint32_t* err;
-  void* scratch;  // verify_scratch_bytes
+  uint32_t* arrived;  // kPagedCounters
+  void* scratch;      // verify_scratch_bytes
 };
 size_t verify_scratch_bytes(int batch, int total, int vocab);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);

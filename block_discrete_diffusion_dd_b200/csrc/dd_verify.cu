@@ -10,19 +10,19 @@
 // sum exceeds u_s W.  Accepted tokens and the next one are then distributed
 // as the target's own samples.
 //
-// Four kernels:
+// Three kernels:
 //   scan    one read of all the target's rows: per chunk of 1,024 16-byte
 //           blocks a reference r and the sum of 2^(x c - r), c = log2(e) / tau,
 //           in fp32.  Bound by memory, with the exponentials close behind (one
 //           per entry: 23 us of MUFU time against 30 us of HBM time for 390
-//           bf16 rows of 262,144).
-//   decide  one CTA per sequence merges the chunks of its rows, forms p(x_i)
-//           and takes the first refusal.  A test within kNear of equality is
-//           repeated with a 64-bit sum over the row, so that the decision is
-//           the one exact arithmetic takes: the fp32 exponents are off by at
-//           most 2^-24 |x c| and c by 2^-25 of itself, which moves p by less
-//           than 1e-6 for scores within 30 of each other.
-//   norm    for the one row the next token is drawn at: the 64-bit sums of
+//           bf16 rows of 262,144).  The chunk that finishes a row merges its
+//           chunks, forms p(x_i) and tests it.  A test within kNear of equality
+//           is left open: the fp32 exponents are off by at most 2^-24 |x c| and
+//           c by 2^-25 of itself, which moves p by less than 1e-6 for scores
+//           within 30 of each other.
+//   norm    finds the first refusal, repeating open tests with 64-bit sums over
+//           their rows, so that the decision is the one exact arithmetic takes;
+//           then, for the one row the next token is drawn at, the 64-bit sums of
 //           the target's and the draft's exponentials per chunk of kPick
 //           logits.  The running sum has a border per vocabulary entry (up
 //           to 262,144 of them), and a relative error of e in the weights
@@ -30,9 +30,11 @@
 //           a hundred would land on another token, with 64 bits none does.
 //   pick    the weights' sums per chunk; the last chunk to finish finds the
 //           chunk that holds u_s W and walks it.
-// The last three are latency: each thread asks for all it needs at once, and a
+// The last two are latency: each thread asks for all it needs at once, and a
 // phase is one or two barriers.  Sums are taken in a fixed order, so a call's
 // result does not depend on scheduling.
+#include <algorithm>
+
 #include "dd_paged.cuh"
 
 namespace dd {
@@ -42,10 +44,9 @@ constexpr int kThreads = 256;
 constexpr int kBlocks = 4;               // 16-byte blocks of a thread of the scan
 constexpr int kPer = 8;                  // entries of a thread of norm and pick
 constexpr int kPick = kThreads * kPer;   // logits per norm / pick chunk
-constexpr int kDecideThreads = 1024;
 constexpr double kNear = 1e-5;
 
-// What `decide` hands on about sequence b's draw.
+// What `norm` hands on about sequence b's draw.
 struct Draw {
   int t_row;   // target row
   int d_row;   // draft row, or -1: draw from the target's own distribution
@@ -69,7 +70,9 @@ struct VerifyParams {
   const float *u_accept, *u_sample;
   int32_t *accepted, *tokens;
   float* target_prob;
-  float2* scan;       // [total + batch][scan chunks]: reference, sum
+  float2* scan;       // [total + batch][segments]: reference, sum
+  uint32_t* arrived;  // [kPagedCounters]: chunks done of the rows = i mod their number
+  float* ref;         // [total + batch]: the rows' references
   uint8_t* state;     // [total]: 0 accepted, 1 refused, 2 near
   Draw* draw;         // [batch]
   Part* part;         // [batch][2][pick chunks]
@@ -163,69 +166,137 @@ __device__ __forceinline__ float blocks_max(const uint4 (&v)[kBlocks]) {
 }
 
 // A row is read in aligned 16-byte blocks, whatever its start; entries of the
-// first and the last block that are not the row's count as -inf.
+// first and the last block that are not the row's count as -inf.  A CTA takes
+// `per` chunks of kThreads * kBlocks blocks of one row, the next one's blocks
+// in flight while the exponentials of one are summed.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_scan_kernel(const VerifyParams p, int chunks) {
+__global__ void __launch_bounds__(kThreads)
+    verify_scan_kernel(const VerifyParams p, int segs, int per) {
   constexpr int kE = 16 / sizeof(T);
   __shared__ float2 sm[kThreads / 32];
+  __shared__ int last;
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x / chunks, ch = blockIdx.x % chunks;
+  const int row = blockIdx.x / segs, seg = blockIdx.x % segs;
   const T* x = static_cast<const T*>(p.target) + row * p.target_stride;
   const int skew = (int)(reinterpret_cast<uintptr_t>(x) & 15u) / (int)sizeof(T);
   const uint4* base = reinterpret_cast<const uint4*>(x - skew);
   const int blocks = (p.vocab + skew + kE - 1) / kE;
   const bool whole = (p.vocab + skew) % kE == 0;  // the last block is all the row's
-  const int b0 = ch * kThreads * kBlocks + threadIdx.x;
-  uint4 v[kBlocks];
+  const int chunk0 = seg * per;
+  auto load = [&](int ch, uint4 (&v)[kBlocks]) {
 #pragma unroll
-  for (int i = 0; i < kBlocks; ++i) {
-    const int b = b0 + i * kThreads;
-    constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-    v[i] = make_uint4(kNone, kNone, kNone, kNone);
-    if ((b > 0 || skew == 0) && (b < blocks - 1 || (b == blocks - 1 && whole))) {
-      v[i] = __ldcs(base + b);
-    } else if (b < blocks) {  // an end of the row: entry by entry
-      uint32_t w[4] = {kNone, kNone, kNone, kNone};
+    for (int i = 0; i < kBlocks; ++i) {
+      const int b = (ch * kBlocks + i) * kThreads + threadIdx.x;
+      constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+      v[i] = make_uint4(kNone, kNone, kNone, kNone);
+      if ((b > 0 || skew == 0) && (b < blocks - 1 || (b == blocks - 1 && whole))) {
+        v[i] = __ldcs(base + b);
+      } else if (b < blocks) {  // an end of the row: entry by entry
+        uint32_t w[4] = {kNone, kNone, kNone, kNone};
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const int at = b * kE + e - skew;
-        if (at < 0 || at >= p.vocab) continue;
-        if constexpr (sizeof(T) == 2) {
-          const uint32_t bits = __ldg(x + at);
-          w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (bits << 16) : (w[e / 2] & 0xffff0000u) | bits;
-        } else {
-          w[e] = __ldg(x + at);
+        for (int e = 0; e < kE; ++e) {
+          const int at = b * kE + e - skew;
+          if (at < 0 || at >= p.vocab) continue;
+          if constexpr (sizeof(T) == 2) {
+            const uint32_t bits = __ldg(x + at);
+            w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (bits << 16) : (w[e / 2] & 0xffff0000u) | bits;
+          } else {
+            w[e] = __ldg(x + at);
+          }
         }
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  }
-  // each warp has a reference of its own
+  };
+  // each warp has a reference of its own, which follows its maximum
   const float c = (float)p.c;
-  const float ref = safe_max(warp_max(blocks_max<T>(v))) * c;
-  const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+  const float2 c2 = make_float2(c, c);
+  float ref = safe_max(-INFINITY) * c;
   float2 s2 = make_float2(0.f, 0.f);
+  uint4 next[kBlocks];
+  load(chunk0, next);
+  for (int ch = 0; ch < per && (chunk0 + ch) * kThreads * kBlocks < blocks; ++ch) {
+    uint4 v[kBlocks];
 #pragma unroll
-  for (int i = 0; i < kBlocks; ++i) {
-    float e[kE];
-    unpack<T>(v[i], e);
+    for (int i = 0; i < kBlocks; ++i) v[i] = next[i];
+    if (ch + 1 < per) load(chunk0 + ch + 1, next);
+    const float top = fmaxf(ref, warp_max(blocks_max<T>(v)) * c);
+    const float f = ex2_approx(ref - top);
+    s2 = __fmul2_rn(s2, make_float2(f, f));
+    ref = top;
+    const float2 r2 = make_float2(-ref, -ref);
 #pragma unroll
-    for (int k = 0; k < kE; k += 2) {
-      const float2 d = __ffma2_rn(make_float2(e[k], e[k + 1]), c2, r2);
-      s2 = __fadd2_rn(s2, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
+    for (int i = 0; i < kBlocks; ++i) {
+      float e[kE];
+      unpack<T>(v[i], e);
+#pragma unroll
+      for (int k = 0; k < kE; k += 2) {
+        const float2 d = __ffma2_rn(make_float2(e[k], e[k + 1]), c2, r2);
+        s2 = __fadd2_rn(s2, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
+      }
     }
   }
   const float s = warp_sum(s2.x + s2.y);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float2(ref, s);
   __syncthreads();
+  const int cls = row % (int)kPagedCounters, rows = p.total + p.batch;
   if (threadIdx.x == 0) {
     float top = sm[0].x, sum = 0.f;
 #pragma unroll
     for (int i = 1; i < kThreads / 32; ++i) top = fmaxf(top, sm[i].x);
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) sum = fmaf(sm[i].y, exp2f(sm[i].x - top), sum);
-    p.scan[(int64_t)row * chunks + ch] = make_float2(top, sum);
+    p.scan[(int64_t)row * segs + seg] = make_float2(top, sum);
+    // rows that share a counter are finished together (there are
+    // kPagedCounters of them, so mostly that is one row)
+    __threadfence();
+    const uint32_t all = (uint32_t)(((rows - 1 - cls) / (int)kPagedCounters + 1) * segs);
+    last = atomicAdd(&p.arrived[cls], 1u) == all - 1;
+    if (last) p.arrived[cls] = 0;  // for the next call
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = cls + warp * (int)kPagedCounters; r < rows; r += kThreads / 32 * (int)kPagedCounters) {
+    // the sequence whose rows cu[b] + b .. cu[b + 1] + b hold r
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu + mid) + mid <= r) lo = mid;
+      else hi = mid;
+    }
+    const int q0 = __ldg(p.cu + lo), q1 = __ldg(p.cu + lo + 1), t = r - lo;
+    const bool drafted = q0 >= 0 && q1 <= p.total && t >= q0 && t < q1;
+    int tok = -1;
+    double bar = 0;
+    if (drafted) {
+      tok = __ldg(p.draft_tokens + t);
+      bar = (double)__ldg(p.u_accept + t) * (double)__ldg(p.draft_conf + t);
+    }
+    const bool in = (uint32_t)tok < (uint32_t)p.vocab;
+    const float x1 = in ? logit(static_cast<const T*>(p.target) + r * p.target_stride, tok) : 0.f;
+    const float2* sc = p.scan + (int64_t)r * segs;
+    const float2 mine = lane < segs ? __ldcg(sc + lane) : make_float2(-INFINITY, 0.f);
+    float top = mine.x;
+    for (int k = lane + 32; k < segs; k += 32) top = fmaxf(top, __ldcg(sc + k).x);
+    top = warp_max(top);
+    double sum = (double)mine.y * exp2f(mine.x - top);
+    for (int k = lane + 32; k < segs; k += 32) {
+      const float2 v = __ldcg(sc + k);
+      sum += (double)v.y * exp2f(v.x - top);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) {
+      p.ref[r] = top;
+      if (drafted) {
+        if (!in) atomicOr(p.err, kDevErrBounds);
+        const double pr = in && sum > 0 ? exp2((double)x1 * (double)c - (double)top) / sum : 0;
+        p.target_prob[t] = (float)pr;
+        p.state[t] = pr == 0 ? 1 : fabs(bar - pr) <= kNear * pr ? 2 : bar < pr ? 0 : 1;
+      }
+    }
   }
 }
 
@@ -234,93 +305,63 @@ __global__ void __launch_bounds__(kThreads) verify_scan_kernel(const VerifyParam
 template <typename T>
 __device__ double exact_prob(const T* x, int vocab, double c, double ref, int tok, double* smd) {
   double s = 0;
-  for (int v = threadIdx.x; v < vocab; v += kDecideThreads) s += exp2((double)logit(x, v) * c - ref);
+  for (int v = threadIdx.x; v < vocab; v += kThreads) s += exp2((double)logit(x, v) * c - ref);
   s = warp_sum(s);
   if ((threadIdx.x & 31) == 0) smd[threadIdx.x >> 5] = s;
   __syncthreads();
   s = 0;
-  for (int i = 0; i < kDecideThreads / 32; ++i) s += smd[i];
+  for (int i = 0; i < kThreads / 32; ++i) s += smd[i];
   __syncthreads();
   return exp2((double)logit(x, tok) * c - ref) / s;
 }
 
+// The draw of sequence b: its first refusal, by every CTA of `norm` alike; the
+// first of them (`mine`) also writes the outputs that follow from it.
 template <typename T>
-__global__ void __launch_bounds__(kDecideThreads)
-    verify_decide_kernel(const VerifyParams p, int chunks) {
-  __shared__ double smd[kDecideThreads / 32];
+__device__ Draw find_draw(const VerifyParams& p, int b, bool mine) {
+  __shared__ double smd[kThreads / 32];
   __shared__ int first;
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q0 = p.cu[b], q1 = p.cu[b + 1];
   Draw dr{0, -1, -1, 0};
+  const int q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1);
   if (q0 < 0 || q1 < q0 || q1 > p.total) {
-    if (threadIdx.x == 0) {
+    if (mine && threadIdx.x == 0) {
       atomicOr(p.err, kDevErrBounds);
       p.accepted[b] = 0;
       p.draw[b] = dr;
     }
-    return;
+    return dr;
   }
   const int k = q1 - q0;
-  auto row_of = [&](int i) {
-    return static_cast<const T*>(p.target) + (int64_t)(q0 + b + i) * p.target_stride;
-  };
-  // the row's reference and sum, from its chunks, in every lane
-  auto merge = [&](int i, float& ref) {
-    const float2* sc = p.scan + (int64_t)(q0 + b + i) * chunks;
-    const float2 mine = lane < chunks ? sc[lane] : make_float2(-INFINITY, 0.f);
-    ref = mine.x;
-    for (int c = lane + 32; c < chunks; c += 32) ref = fmaxf(ref, sc[c].x);
-    ref = warp_max(ref);
-    double s = (double)mine.y * exp2f(mine.x - ref);
-    for (int c = lane + 32; c < chunks; c += 32) s += (double)sc[c].y * exp2f(sc[c].x - ref);
-    return warp_sum(s);
-  };
-  const float c1 = (float)p.c;  // the scan's own factor
-  for (int i = warp; i < k; i += kDecideThreads / 32) {
-    const int tok = p.draft_tokens[q0 + i];
-    const double bar = (double)p.u_accept[q0 + i] * (double)p.draft_conf[q0 + i];
-    const bool in = (uint32_t)tok < (uint32_t)p.vocab;
-    const float x = in ? logit(row_of(i), tok) : -INFINITY;
-    float ref;
-    const double s = merge(i, ref);
-    if (lane == 0) {
-      if (!in) atomicOr(p.err, kDevErrBounds);
-      const double pr = s > 0 ? exp2((double)x * (double)c1 - (double)ref) / s : 0;
-      p.target_prob[q0 + i] = (float)pr;
-      p.state[q0 + i] = pr == 0 ? 1 : fabs(bar - pr) <= kNear * pr ? 2 : bar < pr ? 0 : 1;
-    }
-  }
-  __syncthreads();
   int n = 0;
-  while (true) {  // the first row that is not accepted; near ones are decided in 64 bits
+  while (true) {
     if (threadIdx.x == 0) first = k;
     __syncthreads();
-    for (int i = n + threadIdx.x; i < k; i += kDecideThreads)
+    for (int i = n + threadIdx.x; i < k; i += kThreads)
       if (p.state[q0 + i] != 0) {
         atomicMin(&first, i);
         break;
       }
     __syncthreads();
     n = first;
-    __syncthreads();
     if (n == k || p.state[q0 + n] == 1) break;
-    float ref;
-    merge(n, ref);
-    const double pr = exact_prob(row_of(n), p.vocab, p.c, (double)ref, p.draft_tokens[q0 + n], smd);
+    const int row = q0 + b + n;
+    const double pr = exact_prob(static_cast<const T*>(p.target) + row * p.target_stride, p.vocab,
+                                 p.c, (double)p.ref[row], p.draft_tokens[q0 + n], smd);
     if (!((double)p.u_accept[q0 + n] * (double)p.draft_conf[q0 + n] < pr)) break;
     ++n;
   }
-  for (int i = threadIdx.x; i <= k; i += kDecideThreads)
-    if (i != n) p.tokens[q0 + b + i] = i < n ? p.draft_tokens[q0 + i] : -1;
-  if (threadIdx.x == 0) {
-    p.accepted[b] = n;
-    dr.t_row = q0 + b + n;
-    dr.d_row = n < k ? q0 + n : -1;
-    dr.out = q0 + b + n;
-    p.draw[b] = dr;
+  dr.t_row = q0 + b + n;
+  dr.d_row = n < k ? q0 + n : -1;
+  dr.out = q0 + b + n;
+  if (mine) {
+    for (int i = threadIdx.x; i <= k; i += kThreads)
+      if (i != n) p.tokens[q0 + b + i] = i < n ? p.draft_tokens[q0 + i] : -1;
+    if (threadIdx.x == 0) {
+      p.accepted[b] = n;
+      p.draw[b] = dr;
+    }
   }
+  return dr;
 }
 
 // This thread's kPer consecutive entries of a chunk: bits of one or two
@@ -362,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) verify_norm_kernel(const VerifyParam
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / chunks, ch = blockIdx.x % chunks;
-  const Draw dr = p.draw[b];
+  const Draw dr = find_draw<T>(p, b, ch == 0);
   if (dr.out < 0) return;
   float xt[kPer], xd[kPer];
   load_rows<T>(p, dr, ch, xt, xd);
@@ -546,13 +587,13 @@ int pick_chunks(int vocab) { return (vocab + kPick - 1) / kPick; }
 
 template <typename T>
 cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
-  const int sc = scan_chunks<T>(p.vocab), pc = pick_chunks(p.vocab);
-  cudaError_t e = launch_pdl(verify_scan_kernel<T>, dim3((p.total + p.batch) * sc), dim3(kThreads),
-                             0, stream, p, sc);
-  note_launch();
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(verify_decide_kernel<T>, dim3(p.batch), dim3(kDecideThreads), 0, stream, p,
-                 sc);
+  // several chunks per CTA once there are many more than the SMs hold (up to
+  // eight CTAs each), so that what a CTA does besides reading is done less often
+  const int sc = scan_chunks<T>(p.vocab), pc = pick_chunks(p.vocab), rows = p.total + p.batch;
+  const int per = (int)std::min<int64_t>(8, std::max<int64_t>(1, (int64_t)rows * sc / (148 * 16)));
+  const int segs = (sc + per - 1) / per;
+  cudaError_t e = launch_pdl(verify_scan_kernel<T>, dim3(rows * segs), dim3(kThreads), 0, stream, p,
+                             segs, per);
   note_launch();
   if (e != cudaSuccess) return e;
   e = launch_pdl(verify_norm_kernel<T>, dim3(p.batch * pc), dim3(kThreads), 0, stream, p, pc);
@@ -567,7 +608,8 @@ cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
 
 size_t verify_scratch_bytes(int batch, int total, int vocab) {
   const size_t sc = scan_chunks<uint32_t>(vocab), pc = pick_chunks(vocab);  // fp32: the more
-  return align16((size_t)(total + batch) * sc * sizeof(float2)) + align16((size_t)total) +
+  return align16((size_t)(total + batch) * sc * sizeof(float2)) +
+         align16((size_t)(total + batch) * sizeof(float)) + align16((size_t)total) +
          align16((size_t)batch * sizeof(Draw)) + (size_t)batch * 2 * pc * sizeof(Part) +
          (size_t)batch * pc * sizeof(double);
 }
@@ -592,10 +634,13 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   p.tokens = a.tokens;
   p.target_prob = a.target_prob;
   p.err = a.err;
+  p.arrived = a.arrived;
   const size_t sc = scan_chunks<uint32_t>(a.vocab), pc = pick_chunks(a.vocab);
   uint8_t* s = static_cast<uint8_t*>(a.scratch);
   p.scan = reinterpret_cast<float2*>(s);
   s += align16((size_t)(a.total + a.batch) * sc * sizeof(float2));
+  p.ref = reinterpret_cast<float*>(s);
+  s += align16((size_t)(a.total + a.batch) * sizeof(float));
   p.state = s;
   s += align16((size_t)a.total);
   p.draw = reinterpret_cast<Draw*>(s);

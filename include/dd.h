@@ -506,9 +506,9 @@ DD_API dd_status dd_denoise_block_adaptive_graph_destroy(dd_adaptive_graph graph
  * dd_paged_batch) is taken as empty, a page id outside the pool is never
  * followed, and both latch DD_ERR_DEVICE_BOUNDS in the workspace.  Besides
  * the error word their workspaces hold 4 KB of counters, which every
- * completed call leaves cleared and dd_verify_draft does not touch: calls of
- * this family, of any shape, may share a workspace (cleared once with
- * dd_workspace_init) as long as they do not overlap in time. */
+ * completed call leaves cleared: calls of this family, of any shape, may
+ * share a workspace (cleared once with dd_workspace_init) as long as they do
+ * not overlap in time. */
 
 /* A cache of pages.  One page holds page_size consecutive positions of one
  * sequence, for every kv head.
