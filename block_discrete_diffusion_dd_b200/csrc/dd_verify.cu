@@ -545,8 +545,14 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParam
     }
     at += wi;
   }
-  if (pass >= 0) atomicMin(&s_tok, pass);
-  if (mass >= 0) atomicMax(&s_chunk, mass);
+  // (one candidate per warp: thread order is vocabulary order)
+  auto offer = [&](int lowest, int highest) {
+    const uint32_t lo = __ballot_sync(0xffffffffu, lowest >= 0);
+    const uint32_t hi = __ballot_sync(0xffffffffu, highest >= 0);
+    if (lo && lane == __ffs(lo) - 1) atomicMin(&s_tok, lowest);
+    if (hi && lane == 31 - __clz(hi)) atomicMax(&s_chunk, highest);
+  };
+  offer(pass, mass);
   __syncthreads();
   const int c = s_tok < p.vocab ? s_tok : s_chunk;
   if (c < 0) {  // no mass at all: every logit of the target's row is -inf
@@ -558,19 +564,16 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParam
   load_rows<T>(p, dr, c, xt, xd);
   double sum;
   at = prefix(weigh(rest, w), smd[2], sum);  // (its barriers publish s_bar)
-  int last = -1;
+  int found = -1, last = -1;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     at += w[e];
     if (w[e] > 0) {
       last = c * kPick + threadIdx.x * kPer + e;
-      if (at > s_bar) {
-        atomicMin(&s_tok, last);
-        break;
-      }
+      if (found < 0 && at > s_bar) found = last;
     }
   }
-  if (last >= 0) atomicMax(&s_chunk, last);
+  offer(found, last);
   __syncthreads();
   // (rounding may leave the bar at the chunk's end: its last entry with mass)
   if (threadIdx.x == 0) p.tokens[dr.out] = s_tok < p.vocab ? s_tok : s_chunk;
