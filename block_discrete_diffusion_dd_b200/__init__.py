@@ -677,39 +677,45 @@ def _need(ok: bool, what: str):
 
 
 class _on:
-    """Makes `device` the current one around a call on its tensors; as a value
-    of `with`, the stream to launch on: `stream`, or the device's current one
-    (its raw handle: a torch.cuda.Stream object costs more than a launch)."""
-    __slots__ = ("_guard", "_stream")
+    """Makes `device`, and `stream` if one is given, the current ones around a
+    call, so that what the call allocates belongs to the stream that it runs
+    on; `raw` is that stream's handle (a torch.cuda.Stream object costs more
+    than a launch)."""
+    __slots__ = ("raw", "_guard", "_caller")
 
     def __init__(self, device, stream):
-        self._guard = (None if device.index == torch._C._cuda_getDevice()
-                       else torch.cuda.device(device))
-        self._stream = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-                        else stream.cuda_stream)
+        self._caller = None
+        if stream is None:
+            self._guard = (None if device.index == torch._C._cuda_getDevice()
+                           else torch.cuda.device(device))
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            _need(stream.device == device, f"a stream of {stream.device} for tensors on {device}")
+            self._caller = torch.cuda.current_stream(device)
+            self._guard = torch.cuda.stream(stream)
+            self.raw = stream.cuda_stream
 
     def __enter__(self):
         if self._guard is not None:
             self._guard.__enter__()
-        return self._stream
+        return self
 
     def __exit__(self, *exc):
         if self._guard is not None:
             self._guard.__exit__(*exc)
+
+    def lend(self, t: torch.Tensor) -> torch.Tensor:
+        """A tensor allocated here and returned to a caller on another stream:
+        its memory is not reused before that stream is done with it either."""
+        if self._caller is not None:
+            t.record_stream(self._caller)
+        return t
 
 
 def _own(workspace: torch.Tensor, device):
     if workspace.device != device or workspace.dtype != torch.uint8:
         raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected "
                          f"torch.uint8 on {device}")
-
-
-def _lent(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor allocated here, on the current stream, for a call on `stream`:
-    its memory is not reused before that stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def _packed(t: torch.Tensor, heads: int, dim: int, dtype, device, what: str) -> int:
@@ -755,7 +761,7 @@ class PagedCache:
                 _dense(t, k.shape[:3], torch.uint8, k.device, what)
         else:
             _need(k_scale is None and v_scale is None, "only an E4M3 cache has scales")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = k, v, k_scale, v_scale
         self.num_pages, self.heads_kv, self.page_size, self.head_dim = k.shape
 
         def at(t):
@@ -764,6 +770,11 @@ class PagedCache:
         self._c = _PagedCacheC(self.num_pages, self.page_size, self.heads_kv, self.head_dim, code,
                                at(k), at(v), at(k_scale), at(v_scale))
         self._ref = ctypes.byref(self._c)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
 
 def new_paged_cache(num_pages: int, page_size: int, heads_kv: int, head_dim: int,
@@ -785,21 +796,34 @@ class PagedBatch:
 
     def __init__(self, page_table: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor,
                  max_new: int):
+        self.max_new = max_new
+        self._take(page_table, cu_new, kv_len)
+
+    def _take(self, page_table, cu_new, kv_len):
         _need(page_table.dim() == 2, "page_table must be [batch, max_pages]")
         B, pages = page_table.shape
-        self.device = page_table.device
         _need(page_table.is_cuda, "page_table must be a CUDA tensor")
-        _dense(page_table, (B, pages), torch.int32, self.device, "page_table")
-        _dense(cu_new, (B + 1,), torch.int32, self.device, "cu_new")
-        _dense(kv_len, (B,), torch.int32, self.device, "kv_len")
-        self.page_table, self.cu_new, self.kv_len, self.max_new = page_table, cu_new, kv_len, max_new
-        self.batch = B
+        dev = page_table.device
+        _dense(page_table, (B, pages), torch.int32, dev, "page_table")
+        _dense(cu_new, (B + 1,), torch.int32, dev, "cu_new")
+        _dense(kv_len, (B,), torch.int32, dev, "kv_len")
+        self.device, self.batch, self._tensors = dev, B, (page_table, cu_new, kv_len)
         self._struct = _PagedBatchC(B, pages, 0, 0, page_table.data_ptr(), cu_new.data_ptr(),
                                     kv_len.data_ptr())
 
+    page_table = property(lambda self: self._tensors[0],
+                          lambda self, t: self._take(t, self.cu_new, self.kv_len))
+    cu_new = property(lambda self: self._tensors[1],
+                      lambda self, t: self._take(self.page_table, t, self.kv_len))
+    kv_len = property(lambda self: self._tensors[2],
+                      lambda self, t: self._take(self.page_table, self.cu_new, t))
+
     def _c(self, total_new: int):
         c = self._struct
-        c.total_new, c.max_new = total_new, self.max_new
+        if c.total_new != total_new or c.max_new != self.max_new:
+            # a new one: a call on another host thread may be reading the last
+            c = self._struct = _PagedBatchC(c.batch, c.max_pages, total_new, self.max_new,
+                                            c.page_table, c.cu_new, c.kv_len)
         return c
 
 
@@ -812,13 +836,13 @@ def cache_append(cache: PagedCache, batch: PagedBatch, k_new: torch.Tensor, v_ne
     ks = _packed(k_new, cache.heads_kv, cache.head_dim, torch.bfloat16, dev, "k_new")
     vs = _packed(v_new, cache.heads_kv, cache.head_dim, torch.bfloat16, dev, "v_new")
     _need(k_new.shape[0] == v_new.shape[0], "k_new and v_new have different numbers of rows")
-    with _on(dev, stream) as st:
+    with _on(dev, stream) as on:
         if workspace is None:
-            workspace = _lent(new_workspace(int(lib.dd_cache_workspace()), dev, stream), stream)
+            workspace = new_workspace(int(lib.dd_cache_workspace()), dev, stream)
         _own(workspace, dev)
         _check(lib.dd_cache_append(cache._ref, batch._c(k_new.shape[0]), k_new.data_ptr(), ks,
                                    v_new.data_ptr(), vs, workspace.data_ptr(), workspace.numel(),
-                                   st))
+                                   on.raw))
 
 
 def cache_read(cache: PagedCache, page_table: torch.Tensor, cu_prefix: torch.Tensor,
@@ -835,19 +859,19 @@ def cache_read(cache: PagedCache, page_table: torch.Tensor, cu_prefix: torch.Ten
     total = k_out.shape[0] if total is None else int(total)
     _need(total >= 0, f"total={total}")
     shape = (total, cache.heads_kv, cache.head_dim)
-    if k_out is None:
-        k_out = _lent(torch.empty(shape, dtype=torch.bfloat16, device=dev), stream)
-    if v_out is None:
-        v_out = _lent(torch.empty(shape, dtype=torch.bfloat16, device=dev), stream)
-    _dense(k_out, shape, torch.bfloat16, dev, "k_out")
-    _dense(v_out, shape, torch.bfloat16, dev, "v_out")
-    with _on(dev, stream) as st:
+    with _on(dev, stream) as on:
+        if k_out is None:
+            k_out = on.lend(torch.empty(shape, dtype=torch.bfloat16, device=dev))
+        if v_out is None:
+            v_out = on.lend(torch.empty(shape, dtype=torch.bfloat16, device=dev))
+        _dense(k_out, shape, torch.bfloat16, dev, "k_out")
+        _dense(v_out, shape, torch.bfloat16, dev, "v_out")
         if workspace is None:
-            workspace = _lent(new_workspace(int(lib.dd_cache_workspace()), dev, stream), stream)
+            workspace = new_workspace(int(lib.dd_cache_workspace()), dev, stream)
         _own(workspace, dev)
         _check(lib.dd_cache_read(cache._ref, B, pages, page_table.data_ptr(),
                                  cu_prefix.data_ptr(), total, k_out.data_ptr(), v_out.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel(), st))
+                                 workspace.data_ptr(), workspace.numel(), on.raw))
     return k_out, v_out
 
 
@@ -868,22 +892,21 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, batch: PagedBatch,
     T, Hq = q.shape[0], q.shape[1]
     qs = _packed(q, Hq, D, torch.bfloat16, dev, "q")
     _need(batch.device == dev, "the batch and the cache are on different devices")
-    if out is None:
-        out = _lent(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev), stream)
-    _dense(out, (T, Hq, D), torch.bfloat16, dev, "out")
-    if want_lse and lse is None:
-        lse = _lent(torch.empty((T, Hq), dtype=torch.float32, device=dev), stream)
-    if lse is not None:
-        _dense(lse, (T, Hq), torch.float32, dev, "lse")
-    with _on(dev, stream) as st:
+    with _on(dev, stream) as on:
+        if out is None:
+            out = on.lend(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev))
+        _dense(out, (T, Hq, D), torch.bfloat16, dev, "out")
+        if want_lse and lse is None:
+            lse = on.lend(torch.empty((T, Hq), dtype=torch.float32, device=dev))
+        if lse is not None:
+            _dense(lse, (T, Hq), torch.float32, dev, "lse")
         if workspace is None:
-            workspace = _lent(new_workspace(paged_attn_workspace_bytes(cache, batch, T, Hq), dev,
-                                            stream), stream)
+            workspace = new_workspace(paged_attn_workspace_bytes(cache, batch, T, Hq), dev, stream)
         _own(workspace, dev)
         _check(lib.dd_paged_attn(cache._ref, batch._c(T), Hq, q.data_ptr(), qs,
                                  float(scale if scale is not None else D ** -0.5), int(causal),
                                  out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel(), st))
+                                 workspace.data_ptr(), workspace.numel(), on.raw))
     return out, lse
 
 
@@ -929,15 +952,14 @@ def verify_draft(target_logits: torch.Tensor, draft_logits: torch.Tensor,
                            (u_sample, B, torch.float32, "u_sample")):
         _dense(t, (n,), dt, dev, what)
     o = outputs
-    if o is None:
-        o = {k: _lent(t, stream) for k, t in verify_draft_outputs(B, T, dev).items()}
-    for name, n, dt in (("accepted", B, torch.int32), ("tokens", T + B, torch.int32),
-                        ("target_prob", T, torch.float32)):
-        _dense(o[name], (n,), dt, dev, name)
-    with _on(dev, stream) as st:
+    with _on(dev, stream) as on:
+        if o is None:
+            o = {k: on.lend(t) for k, t in verify_draft_outputs(B, T, dev).items()}
+        for name, n, dt in (("accepted", B, torch.int32), ("tokens", T + B, torch.int32),
+                            ("target_prob", T, torch.float32)):
+            _dense(o[name], (n,), dt, dev, name)
         if workspace is None:
-            workspace = _lent(new_workspace(verify_draft_workspace_bytes(B, T, V), dev, stream),
-                              stream)
+            workspace = new_workspace(verify_draft_workspace_bytes(B, T, V), dev, stream)
         prm = VerifyParams(float(temperature), float(draft_temperature))
         _own(workspace, dev)
         _check(lib.dd_verify_draft(
@@ -946,7 +968,7 @@ def verify_draft(target_logits: torch.Tensor, draft_logits: torch.Tensor,
             zd[0] if T > 1 else V, draft_tokens.data_ptr(),
             draft_conf.data_ptr(), cu_draft.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(),
             o["accepted"].data_ptr(), o["tokens"].data_ptr(), o["target_prob"].data_ptr(),
-            workspace.data_ptr(), workspace.numel(), st))
+            workspace.data_ptr(), workspace.numel(), on.raw))
     return o
 
 

@@ -546,7 +546,7 @@ typedef struct {
  * A row is impossible, and taken as empty, unless 0 <= cu_new[b] <=
  * cu_new[b+1] <= total_new, n <= max_new and 0 <= kv_len[b] <=
  * max_pages * page_size.  kv_len[b] < n is possible: positions below 0 are
- * not stored and see nothing. */
+ * not stored, and under a causal mask they see nothing. */
 typedef struct {
   int batch, max_pages, total_new, max_new;
   const int32_t *page_table, *cu_new, *kv_len;

@@ -501,3 +501,47 @@ def test_timeout_is_reported_and_the_next_call_is_right(kind, new):
     assert err.value.status == 5  # DD_ERR_DEVICE_TIMEOUT
     for _ in range(2):
         _check_attn(q, cache, k64, v64, pr)
+
+
+def test_outputs_belong_to_the_calls_stream():
+    # memory freed on the current stream with work on it still pending is not
+    # what a call on another stream gets for its outputs
+    pr = ref.problem((3, 60), (100, 900), 16, seed=4)
+    cache, _, _ = _pool(pr, 2, 64, "bf16")
+    q, batch = _normal((63, 8, 64), 5).to(DEV), _batch(pr)
+    ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, 63, 8))
+    want, want_lse = dd.paged_attn(q, cache, batch, want_lse=True, workspace=ws)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = [torch.empty_like(want), torch.empty_like(want_lse)]
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for t in held:
+        t.fill_(7)
+    del held, t
+    out, lse = dd.paged_attn(q, cache, batch, want_lse=True, workspace=ws, stream=side)
+    torch.cuda.synchronize()
+    dd.query_device_error(ws)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_batch_arrays_and_totals_may_change():
+    pr = ref.problem((1, 4), (50, 200), 16, seed=6)
+    cache, k64, v64 = _pool(pr, 2, 64, "bf16")
+    q, batch = _normal((5, 4, 64), 7).to(DEV), _batch(pr)
+    _check_attn(q.cpu(), cache, k64, v64, pr, batch=batch)
+    # another tensor of lengths in place of the first, which is gone
+    batch.kv_len = batch.kv_len - 3
+    torch.full((2,), 1 << 28, dtype=torch.int32, device=DEV)
+    pr.lens = batch.kv_len.cpu().tolist()
+    _check_attn(q.cpu(), cache, k64, v64, pr, batch=batch)
+    for name, bad in (("kv_len", batch.kv_len[:1]), ("cu_new", batch.cu_new.long()),
+                      ("page_table", batch.page_table[0])):
+        with pytest.raises(ValueError):
+            setattr(batch, name, bad)
+    # what one call was given does not change under it
+    five, seven = batch._c(5), batch._c(7)
+    assert (five.total_new, seven.total_new) == (5, 7)
+    with pytest.raises(ValueError):
+        dd.paged_attn(q.cpu(), cache, batch)
+    with pytest.raises(AttributeError):
+        cache.k = cache.v
