@@ -1,7 +1,7 @@
 // dd_abi.cu -- the extern "C" boundary of libdd (declared in include/dd.h):
 // argument validation (always before any launch), launch planning, workspace
 // carving, error reporting and the block loop.  All device work happens in
-// the kernels of dd_sampler.cu, dd_attn_tc.cu and dd_attn_simt.cu.
+// the kernels of the other .cu files.
 #include <cmath>
 #include <utility>
 #include <vector>

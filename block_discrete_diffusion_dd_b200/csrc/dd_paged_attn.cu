@@ -29,18 +29,32 @@
 //            keep the barriers' count.
 //   TMA warp one lane per 8-key group looks the page up; a page's share of the
 //            tile is one box of the tensor map.
-//   MMA warp issues every MMA from one elected lane.  Two S buffers: with two
-//            query tiles one each, in the order PV_0(j) S_0(j+1) PV_1(j)
-//            S_1(j+1); with one query tile (a few rows: decoding) they
-//            alternate, S(j+2) behind PV(j), so that a softmax never waits
-//            for an S product.
+//   MMA warp issues every MMA from one elected lane, so that the tensor core
+//            works ahead of the softmax.  One query tile: two S buffers, used
+//            in turn, S(j+2) behind PV(j).  Two query tiles with P in columns
+//            of its own (kSep): S_0 and S_1 of a key tile as soon as the
+//            softmax has loaded what lay in the buffer, PV_q(j) when its P is
+//            written.  Two query tiles with P where S was: PV_0(j) S_0(j+1)
+//            PV_1(j) S_1(j+1).
 //   convert  (E4M3 cache) expands the 8-bit tiles to bf16 operands: code times
 //            2^e, exact in bf16, so that the products see exactly what the
 //            cache stands for.  The scale bytes follow the page by cp.async.
-// The tensor core runs one thread's MMAs in issue order.  With two query
-// tiles S_q(j) complete therefore means PV_q(j-1) complete, and O may be
-// rescaled; with one, S(j) complete means PV(j-2) complete, and a rescale
-// waits for PV(j-1) on its own barrier.
+// The tensor core runs one thread's MMAs in issue order.  Where P takes S's
+// place with two query tiles, S_q(j) complete therefore means PV_q(j-1)
+// complete, and O may be rescaled; elsewhere a rescale waits for PV(j-1) on
+// its own barrier.
+//
+// What bounds it (D = 128, 148 CTAs): with 256 query rows the softmax, whose
+// 16 warps take about 1.4 us per key tile (loads and maximum 0.3, row
+// reductions 0.3, exponentials 0.7, stores 0.1) and wait 0.3 us for the tensor
+// core, against 1.0 us of tensor-core work: two chunks of 2,048 tokens over
+// 8,192 take 219 to 258 us (the products alone: 135), the tensor pipe being
+// active half of the time.  With an E4M3 cache the conversion: 1.0 us for K
+// and 0.9 us for V of a tile (blocks of 256 tokens of eight sequences with up
+// to 16,384 each: 137 us, from bf16 117).  A short past is bounded by the
+// chain of single steps: the share's search 2.9 us, the Q tile 2.4, the first
+// product 0.8, the epilogue 2.6, and the second kernel about 5 (one block of
+// 256 over 4,096: 28 us).
 //
 // What the cache holds past a sequence's length may be anything, NaN
 // included: masked scores are replaced before they are used, and V rows past
@@ -863,8 +877,15 @@ size_t paged_attn_scratch_bytes(const PagedAttnArgs& a) {
 }
 
 // Up to kFewRows query rows per sequence and kv head, the kernel for few rows
-// (dd_paged_few.cu); up to one tile of them the tensor-core kernel with one
-// query tile; above that with two, so that a key tile serves 256 rows.
+// (dd_paged_few.cu).  Measured against the tensor-core kernel, D = 128, groups
+// of two, 64 sequences of up to 16,384 tokens: E4M3, one token each 195 us
+// against 421, eight tokens (16 rows) 306 against 421; bf16 316 against 377 and
+// 350 against 404.  One sequence of 65,536: bf16 50 against 58 us (16 rows: 58
+// against 65), E4M3 36 against 65 (55 against 69).
+// Above that and up to one tile of rows the tensor-core kernel with one query
+// tile: eight sequences, 32 and 128 rows, bf16 47 and 50 us against 51 and 54
+// with the other, E4M3 54 and 59 against 61 and 67.  More rows: two query
+// tiles, so that a key tile is fetched (and expanded) once for 256 rows.
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   const bool f8 = a.pool.e4m3;
   const int D = a.p.head_dim;

@@ -33,6 +33,13 @@
 // that of 2^(x - m) = w 2^-ev.  The bf16 query is scaled by a power of two per
 // row that puts its largest magnitude in [2^14, 2^15); only what lies 2^28
 // below it loses bits.
+//
+// Measured (D = 128, one token per sequence, group of two): 64 sequences of up
+// to 16,384 tokens, bf16 316 us (6.6 TB/s, the rate of a copy), E4M3 195 us
+// (5.4 TB/s; expanding the codes and the softmax take the issue slots 42% of
+// the time); one sequence of 65,536, bf16 50 us (5.4 TB/s: about 8 us of it are
+// start, merge and end).  Two short sequences at D = 64 take 8.2 us, all of it
+// latency: the launch, the share's search, a key tile, the merge.
 #include "dd_paged_attn.cuh"
 
 namespace dd {

@@ -17,9 +17,10 @@
 //           per entry: 23 us of MUFU time against 30 us of HBM time for 390
 //           bf16 rows of 262,144).  The chunk that finishes a row merges its
 //           chunks, forms p(x_i) and tests it.  A test within kNear of equality
-//           is left open: the fp32 exponents are off by at most 2^-24 |x c| and
-//           c by 2^-25 of itself, which moves p by less than 1e-6 for scores
-//           within 30 of each other.
+//           is left open: an exponent x c - r is off by at most 2^-24 of itself
+//           and c by 2^-25 of itself, which moves p by less than 1e-6 for
+//           scores within 30 of each other and by less than kNear for the
+//           smallest p that u_i conf_i (fp32 factors) can equal.
 //   norm    finds the first refusal, repeating open tests with 64-bit sums over
 //           their rows, so that the decision is the one exact arithmetic takes;
 //           then, for the one row the next token is drawn at, the 64-bit sums of
@@ -33,6 +34,11 @@
 // The last two are latency: each thread asks for all it needs at once, and a
 // phase is one or two barriers.  Sums are taken in a fixed order, so a call's
 // result does not depend on scheduling.
+//
+// Measured, bf16, 262,144 entries: eight sequences with 358 drafted tokens 64
+// us, of which the scan 39 (4.9 TB/s; instructions issued in 60% of the
+// cycles) and norm and pick 25; one sequence with eight drafted tokens 20.5
+// us, nearly all of it the chain of the three kernels.
 #include <algorithm>
 
 #include "dd_paged.cuh"
