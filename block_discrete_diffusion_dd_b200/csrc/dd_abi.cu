@@ -1159,8 +1159,8 @@ PagedPool paged_pool(const dd_paged_cache* c) {
 
 // Rows of one call that a grid of (token, head, K or V) units covers.
 dd_status check_cache_units(int64_t rows, int heads_kv) {
-  if (rows * 2 * heads_kv > INT32_MAX)
-    return fail(DD_ERR_UNSUPPORTED, "tokens * 2 * heads_kv exceeds 2^31");
+  if (rows * 2 * heads_kv > (1 << 30))
+    return fail(DD_ERR_UNSUPPORTED, "tokens * 2 * heads_kv exceeds 2^30");
   return DD_OK;
 }
 
@@ -1297,8 +1297,10 @@ dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch
   return DD_OK;
 }
 
+static constexpr int kMaxDraftVocab = 1 << 30;  // (entry indices, and a chunk past the last)
+
 size_t dd_verify_draft_workspace(int batch, int total, int vocab) {
-  if (batch < 0 || total < 0 || vocab < 1) return 0;
+  if (batch < 0 || total < 0 || vocab < 1 || vocab > kMaxDraftVocab) return 0;
   return kPagedHeader + verify_scratch_bytes(batch, total, vocab);
 }
 
@@ -1322,6 +1324,7 @@ dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int ba
   for (float t : taus)
     if (!std::isfinite(t) || t < 1e-3f)
       return fail(DD_ERR_INVALID_ARG, "temperatures must be finite and >= 1e-3");
+  if (vocab > kMaxDraftVocab) return fail(DD_ERR_UNSUPPORTED, "vocab=%d exceeds 2^30", vocab);
   if (((int64_t)total + batch) * (((int64_t)vocab + 2047) / 2048) > INT32_MAX)
     return fail(DD_ERR_UNSUPPORTED, "rows * chunks exceeds 2^31");
   if (batch == 0) return DD_OK;

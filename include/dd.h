@@ -560,7 +560,7 @@ DD_API size_t dd_cache_workspace(void);
  *                 v_stride elements between tokens (>= heads_kv * head_dim,
  *                 a multiple of 8): views of a fused projection are taken
  *   workspace     >= dd_cache_workspace() bytes, 256-byte aligned
- * A DD_BF16 cache takes the bits as they are.  A DD_E4M3 cache takes, per
+ * total_new * 2 * heads_kv <= 2^30 (as in dd_cache_read).  A DD_BF16 cache takes the bits as they are.  A DD_E4M3 cache takes, per
  * (token, head), with a the largest finite magnitude of its head_dim values,
  * the scale 2^e of the least integer e with a <= 448 * 2^e (within
  * [-120, 120]; 0 when a = 0) and the codes E4M3(x * 2^-e), rounded to
@@ -633,6 +633,7 @@ DD_API dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch
  *   params         temperature, draft_temperature: finite, >= 1e-3
  *   dtype          of both logits: DD_BF16 or DD_F32; finite or -inf
  *   batch, total   B sequences, rows of the packed draft tensors
+ *   vocab          1 .. 2^30
  *   target_logits  [total + B, vocab], target_stride elements between rows:
  *                  sequence b's k_b + 1 rows start at cu_draft[b] + b
  *   draft_logits   [total, vocab], draft_stride elements between rows

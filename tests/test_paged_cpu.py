@@ -172,3 +172,11 @@ def test_reference_quantiser_matches_torch():
     y = x.float() * (2.0 ** -e.float())[..., None]
     assert torch.equal(y.to(torch.float8_e4m3fn).double(), v)
     assert (y.abs().amax(-1) <= 448).all() and (y.abs().amax(-1) > 224).all()
+
+
+def test_sizes_that_indices_cannot_hold(lib):
+    assert _verify(lib, V=(1 << 30) + 1, zs=1 << 31, ds=1 << 31) == UNSUPPORTED
+    assert dd.verify_draft_workspace_bytes(1, 1, (1 << 30) + 1) == 0
+    assert dd.verify_draft_workspace_bytes(1, 1, 1 << 30) > 0
+    # 2 heads: one unit more than 2^30
+    assert _append(lib, batch=_batch(total=(1 << 28) + 1)) == UNSUPPORTED
