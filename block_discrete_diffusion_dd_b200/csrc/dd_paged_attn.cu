@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  find_share<kQT * BM, L::kFixed, L::kMinShare, L::kThreads>(p, &share, warp_sums);
+  find_share<kQT * BM, L::kFixed, L::kMinShare, 0, L::kThreads>(p, &share, warp_sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -8,6 +8,7 @@
 // units of overhead in front of its tiles, and cut into equal shares, one per
 // CTA: every CTA finds its own share from the lengths (a block-wide prefix
 // sum) and walks it.  One wave and no host plan, whatever the lengths are.
+// (Few rows, short sequences and CTAs enough: an item each.)
 // An item that spans CTAs leaves one partial per CTA; at most two of a CTA's
 // items are partial, its first (slot 0) and its last (slot 1).  Partials are
 // merged in CTA order, whoever does it: with many rows per item a second
@@ -177,11 +178,16 @@ __device__ __forceinline__ int64_t row_weight(const Params& p, const ChunkRow& r
   return w;
 }
 
-// kMin: the least share of a CTA.
-template <int kRows, int kFixed, int kMin, int kT>
+// kMin: the least share of a CTA.  kMost > 0 (few rows: one group per sequence
+// and head): where there are no more items than CTAs and none has more than
+// kMost key tiles, CTA c takes item c whole, so that nothing is searched for
+// and nothing has to be merged.
+template <int kRows, int kFixed, int kMin, int kMost, int kT>
 __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
   constexpr int kW = kT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool many = false;  // an item of more than kMost tiles (one barrier serves this too)
+  int item = 0;       // units of an item of this thread's sequence
   // exclusive prefix of v over the block; *all gets the block's sum
   auto scan = [&](int64_t v, int64_t* all) {
     int64_t inc = v;
@@ -191,7 +197,8 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
       if (lane >= o) inc += up;
     }
     if (lane == 31) warp_sums[warp] = inc;
-    __syncthreads();
+    if constexpr (kMost > 0) many = __syncthreads_or(many);
+    else __syncthreads();
     int64_t before = 0, sum = 0;
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
@@ -209,7 +216,10 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
     w = 0;
     if (b < p.b.batch) {
       r = chunk_row(p.b, b, p.err);
-      w = row_weight<kRows, kFixed>(p, r) * p.b.heads_kv;
+      w = row_weight<kRows, kFixed>(p, r);
+      many = w > kMost + kFixed;
+      item = (int)w;
+      w *= p.b.heads_kv;
     }
     at = scan(w, &all);
   };
@@ -218,7 +228,12 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
     weigh(b0);
     total += all;
   }
-  const int ctas = (int)min((int64_t)gridDim.x, (total + kMin - 1) / kMin);
+  // the sequence whose item this CTA takes whole, or -1
+  const int whole = kMost > 0 && !many && p.b.batch <= kT &&
+                            (int64_t)p.b.batch * p.b.heads_kv <= gridDim.x
+                        ? (int)blockIdx.x / p.b.heads_kv
+                        : -1;
+  const int ctas = whole >= 0 ? 0 : (int)min((int64_t)gridDim.x, (total + kMin - 1) / kMin);
   Share s{};
   if (ctas > 0) {
     s.quota = (int64_t)div64(total, (uint32_t)ctas);
@@ -230,7 +245,18 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
   }
   s.total = total;
   s.ctas = ctas;
-  if (threadIdx.x == 0 && s.end == s.pos) *sh = s;
+  if (kMost > 0 && whole >= 0 && whole < p.b.batch) {
+    if ((int)threadIdx.x == whole) {
+      s.end = item;
+      s.b = whole;
+      s.g = (int)blockIdx.x - whole * p.b.heads_kv;
+      s.r = r;
+      *sh = s;
+    }
+    s.end = 0;
+  } else if (threadIdx.x == 0 && s.end == s.pos) {
+    *sh = s;
+  }
   if (s.end > s.pos) {
     int64_t base = 0;
     for (int b0 = 0; b0 < p.b.batch; b0 += kT) {
@@ -406,6 +432,7 @@ template <int D, int kRows, int kFixed, int kT>
 __device__ __forceinline__ void finish_items(const Params& p, Share& share, const Seg& e) {
   __syncthreads();
   if (share.pos == share.end) return;
+  if (share.x <= kFixed && !(e.t0 == 0 && e.t1 > 0 && e.t1 < e.nt)) return;  // whole items only
   if (threadIdx.x == 0) {
     __threadfence();
     // the item the share starts in, with tiles before it and some in it; and

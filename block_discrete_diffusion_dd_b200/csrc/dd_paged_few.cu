@@ -38,8 +38,8 @@
 // to 16,384 tokens, bf16 316 us (6.6 TB/s, the rate of a copy), E4M3 195 us
 // (5.4 TB/s; expanding the codes and the softmax take the issue slots 42% of
 // the time); one sequence of 65,536, bf16 50 us (5.4 TB/s: about 8 us of it are
-// start, merge and end).  Two short sequences at D = 64 take 8.2 us, all of it
-// latency: the launch, the share's search, a key tile, the merge.
+// start, merge and end).  Two short sequences at D = 64 take 6.9 us, all of it
+// latency: the launch, the lengths, the key tiles one after the other.
 #include "dd_paged_attn.cuh"
 
 namespace dd {
@@ -59,6 +59,11 @@ struct Few {
   static constexpr int kWarps = kSmall ? 8 : NT == 1 ? 10 : 8;
   static constexpr int kBlocks = kSmall ? kFewBlocks : 1;
   static constexpr int kRows = 8 * NT;
+  // key tiles of an item that a CTA takes whole where there are CTAs enough:
+  // two sequences of up to 700 tokens (D = 64) 6.9 us against 8.2 shared out; 16
+  // of 512 at D = 128 9.1 against 13.9, of 1,024 13.5 against 18.9 (E4M3: 512
+  // 10.8 against 11.9, but 1,024 16.1 against 14.8)
+  static constexpr int kMostWhole = kF8 ? 6 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kLd = D + 4;  // floats per row of the merge area
   static constexpr int kSmem = kWarps * kRows * (kLd + 2) * 4;
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
   const int g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_trigger();
-  find_share<F::kRows, kFixed, kMinShare, F::kThreads>(p, &share, warp_sums);
+  find_share<F::kRows, kFixed, kMinShare, F::kMostWhole, F::kThreads>(p, &share, warp_sums);
   auto walk = start_walk<F::kRows, kFixed>(p, share);
   const int shift = p.b.page_shift, in_page = (1 << shift) - 1;
   Seg sg{};

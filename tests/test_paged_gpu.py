@@ -545,3 +545,17 @@ def test_batch_arrays_and_totals_may_change():
         dd.paged_attn(q.cpu(), cache, batch)
     with pytest.raises(AttributeError):
         cache.k = cache.v
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,D,new,past", [
+    (2, 128, (1, 1), (767, 1023)),           # the longest items that a CTA takes whole
+    (2, 128, (1, 1), (768, 1024)),           # and one key more
+    (1, 64, (1, 0, 2, 1), (1022, 4, 0, 3)),  # some sequences empty or without new tokens
+    (37, 64, (1, 1, 0, 1), (20, 500, 9, 300)),   # as many items as there may be CTAs of one kind
+    (60, 64, (1, 1, 3, 1, 1), (20, 500, 9, 300, 64)),  # more items than CTAs
+])
+def test_attention_items_taken_whole(kind, H, D, new, past):
+    pr = ref.problem(new, past, 16, seed=H)
+    cache, k64, v64 = _pool(pr, H, D, kind, seed=D)
+    _check_attn(_normal((sum(new), 2 * H, D), 21), cache, k64, v64, pr)
