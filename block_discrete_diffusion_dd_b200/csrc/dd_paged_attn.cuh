@@ -186,6 +186,8 @@ template <int kRows, int kFixed, int kMin, int kMost, int kT>
 __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
   constexpr int kW = kT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool narrow = p.b.batch <= 32;  // one warp's work
+  if (!narrow || warp == 0) {
   bool many = false;  // an item of more than kMost tiles (one barrier serves this too)
   int item = 0;       // units of an item of this thread's sequence
   // exclusive prefix of v over the block; *all gets the block's sum
@@ -195,6 +197,11 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
+    }
+    if (narrow) {
+      many = __any_sync(0xffffffffu, many);
+      *all = __shfl_sync(0xffffffffu, inc, 31);
+      return inc - v;
     }
     if (lane == 31) warp_sums[warp] = inc;
     if constexpr (kMost > 0) many = __syncthreads_or(many);
@@ -283,6 +290,7 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
       }
       base += all;
     }
+  }
   }
   __syncthreads();
 }
