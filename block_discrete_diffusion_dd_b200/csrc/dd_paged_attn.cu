@@ -126,7 +126,7 @@ struct Lay {
   static constexpr int kMinShare = kFixed;
   static_assert(kStagesK <= kMaxStages && kStagesV <= kMaxStages && kRawStages <= kMaxRaw,
                 "barrier arrays");
-  static_assert(kSmem + 3072 <= 232448, "shared memory budget, static part included");
+  static_assert(kSmem + 3 * 1024 <= 227 * 1024, "shared memory budget, static part included");
 };
 
 __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t off) {
