@@ -24,7 +24,7 @@
 //   norm    finds the first refusal, repeating open tests with 64-bit sums over
 //           their rows, so that the decision is the one exact arithmetic takes;
 //           then, for the one row the next token is drawn at, the 64-bit sums of
-//           the target's and the draft's exponentials per chunk of kPick
+//           the target's and the draft's exponentials per chunk of
 //           logits.  The running sum has a border per vocabulary entry (up
 //           to 262,144 of them), and a relative error of e in the weights
 //           moves each border by about e: with fp32 sums one draw in ten to
@@ -37,9 +37,10 @@
 //
 // Measured, bf16, 262,144 entries: eight sequences with 358 drafted tokens 64
 // us, of which the scan 39 (4.9 TB/s; instructions issued in 60% of the
-// cycles) and norm and pick 25; one sequence with eight drafted tokens 20.5
+// cycles) and norm and pick 25; one sequence with eight drafted tokens 17.9
 // us, nearly all of it the chain of the three kernels.
 #include <algorithm>
+#include <type_traits>
 
 #include "dd_paged.cuh"
 
@@ -48,8 +49,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlocks = 4;               // 16-byte blocks of a thread of the scan
-constexpr int kPer = 8;                  // entries of a thread of norm and pick
-constexpr int kPick = kThreads * kPer;   // logits per norm / pick chunk
+// entries of a thread of norm and pick (kPer): 8, or 4 where that makes few
+// chunks (launch_verify_t)
+constexpr int kFew = 4, kMany = 8;
 constexpr double kNear = 1e-5;
 
 // What `norm` hands on about sequence b's draw.
@@ -370,18 +372,26 @@ __device__ Draw find_draw(const VerifyParams& p, int b, bool mine) {
   return dr;
 }
 
-// This thread's kPer consecutive entries of a chunk: bits of one or two
-// 16-byte loads where the row is aligned, entry by entry where not.
-template <typename T>
+// This thread's kPer consecutive entries of a chunk: one or two wide loads
+// where the row is aligned, entry by entry where not.
+template <typename T, int kPer>
 __device__ __forceinline__ void load_entries(const T* x, int v0, int vocab, float (&e)[kPer]) {
   constexpr int kE = 16 / sizeof(T);
   if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0 && v0 + kPer <= vocab) {
+    if constexpr (kPer < kE) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + v0));
+      e[0] = bf16lo(v.x);
+      e[1] = bf16hi(v.x);
+      e[2] = bf16lo(v.y);
+      e[3] = bf16hi(v.y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPer / kE; ++i) {
-      float f[kE];
-      unpack<T>(__ldg(reinterpret_cast<const uint4*>(x + v0) + i), f);
+      for (int i = 0; i < kPer / kE; ++i) {
+        float f[kE];
+        unpack<T>(__ldg(reinterpret_cast<const uint4*>(x + v0) + i), f);
 #pragma unroll
-      for (int k = 0; k < kE; ++k) e[i * kE + k] = f[k];
+        for (int k = 0; k < kE; ++k) e[i * kE + k] = f[k];
+      }
     }
   } else {
 #pragma unroll
@@ -390,19 +400,19 @@ __device__ __forceinline__ void load_entries(const T* x, int v0, int vocab, floa
 }
 
 // What the target's row and the draft's (if any) hold at the draw of b.
-template <typename T>
+template <typename T, int kPer>
 __device__ __forceinline__ void load_rows(const VerifyParams& p, const Draw& dr, int ch,
                                           float (&xt)[kPer], float (&xd)[kPer]) {
-  const int v0 = ch * kPick + threadIdx.x * kPer;
-  load_entries(static_cast<const T*>(p.target) + dr.t_row * p.target_stride, v0, p.vocab, xt);
+  const int v0 = (ch * kThreads + threadIdx.x) * kPer;
+  load_entries<T, kPer>(static_cast<const T*>(p.target) + dr.t_row * p.target_stride, v0, p.vocab, xt);
   if (dr.d_row >= 0)
-    load_entries(static_cast<const T*>(p.draft) + dr.d_row * p.draft_stride, v0, p.vocab, xd);
+    load_entries<T, kPer>(static_cast<const T*>(p.draft) + dr.d_row * p.draft_stride, v0, p.vocab, xd);
   else
 #pragma unroll
     for (int i = 0; i < kPer; ++i) xd[i] = -INFINITY;
 }
 
-template <typename T>
+template <typename T, int kPer>
 __global__ void __launch_bounds__(kThreads) verify_norm_kernel(const VerifyParams p, int chunks) {
   __shared__ float2 smf[kThreads / 32];
   __shared__ Pair smd[kThreads / 32];
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) verify_norm_kernel(const VerifyParam
   const Draw dr = find_draw<T>(p, b, ch == 0);
   if (dr.out < 0) return;
   float xt[kPer], xd[kPer];
-  load_rows<T>(p, dr, ch, xt, xd);
+  load_rows<T, kPer>(p, dr, ch, xt, xd);
   float mt = xt[0], md = xd[0];
 #pragma unroll
   for (int i = 1; i < kPer; ++i) {
@@ -435,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) verify_norm_kernel(const VerifyParam
   }
 }
 
-template <typename T>
+template <typename T, int kPer>
 __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParams p, int chunks) {
   __shared__ float2 smf[kThreads / 32];
   __shared__ Pair smd[3][kThreads / 32];
@@ -450,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParam
   if (dr.out < 0) return;
   const bool drafted = dr.d_row >= 0;
   float xt[kPer], xd[kPer];
-  load_rows<T>(p, dr, ch, xt, xd);
+  load_rows<T, kPer>(p, dr, ch, xt, xd);
   // both rows' maxima and sums from the chunks'
   const Part* part = p.part + (int64_t)b * 2 * chunks;
   const Part none{0, -INFINITY, 0};
@@ -567,7 +577,7 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParam
   }
   if (c == pass) s_bar = bar - before_pass;
   else if (c == mass && s_tok == p.vocab) s_bar = bar - before_mass;
-  load_rows<T>(p, dr, c, xt, xd);
+  load_rows<T, kPer>(p, dr, c, xt, xd);
   double sum;
   at = prefix(weigh(rest, w), smd[2], sum);  // (its barriers publish s_bar)
   int found = -1, last = -1;
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(kThreads) verify_pick_kernel(const VerifyParam
   for (int e = 0; e < kPer; ++e) {
     at += w[e];
     if (w[e] > 0) {
-      last = c * kPick + threadIdx.x * kPer + e;
+      last = (c * kThreads + threadIdx.x) * kPer + e;
       if (found < 0 && at > s_bar) found = last;
     }
   }
@@ -592,31 +602,46 @@ int scan_chunks(int vocab) {
   constexpr int kE = 16 / sizeof(T), kChunk = kThreads * kBlocks * kE;
   return (int)(((int64_t)vocab + kE - 1 + kChunk - 1) / kChunk);
 }
-int pick_chunks(int vocab) { return (vocab + kPick - 1) / kPick; }
+int pick_chunks(int vocab, int per) { return (vocab + kThreads * per - 1) / (kThreads * per); }
 
 template <typename T>
 cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
   // several chunks per CTA once there are many more than the SMs hold (up to
   // eight CTAs each), so that what a CTA does besides reading is done less often
-  const int sc = scan_chunks<T>(p.vocab), pc = pick_chunks(p.vocab), rows = p.total + p.batch;
+  const int sc = scan_chunks<T>(p.vocab), rows = p.total + p.batch;
   const int per = (int)std::min<int64_t>(8, std::max<int64_t>(1, (int64_t)rows * sc / (148 * 16)));
   const int segs = (sc + per - 1) / per;
   cudaError_t e = launch_pdl(verify_scan_kernel<T>, dim3(rows * segs), dim3(kThreads), 0, stream, p,
                              segs, per);
   note_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(verify_norm_kernel<T>, dim3(p.batch * pc), dim3(kThreads), 0, stream, p, pc);
-  note_launch();
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(verify_pick_kernel<T>, dim3(p.batch * pc), dim3(kThreads), 0, stream, p, pc);
-  note_launch();
-  return e;
+  auto draw = [&](auto per_thread) {
+    constexpr int kPer = decltype(per_thread)::value;
+    const int pc = pick_chunks(p.vocab, kPer);
+    cudaError_t e = launch_pdl(verify_norm_kernel<T, kPer>, dim3(p.batch * pc), dim3(kThreads), 0,
+                               stream, p, pc);
+    note_launch();
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(verify_pick_kernel<T, kPer>, dim3(p.batch * pc), dim3(kThreads), 0, stream, p,
+                   pc);
+    note_launch();
+    return e;
+  };
+  // Few chunks (one per SM at most) are waited for, each thread's entries one
+  // after the other: with half as many bf16 entries per thread one sequence of
+  // 262,144 takes 17.9 us (19.5), of 32,000 15.6 (18.3).  Many chunks cost by
+  // their number: eight sequences take 63.8 us with 8 entries, 66.9 with 4 (and
+  // fp32 rows, whose 8 are two loads, 19.6 and 20.4).
+  if constexpr (sizeof(T) == 2)
+    if ((int64_t)p.batch * pick_chunks(p.vocab, kMany) <= 148)
+      return draw(std::integral_constant<int, kFew>{});
+  return draw(std::integral_constant<int, kMany>{});
 }
 
 }  // namespace
 
 size_t verify_scratch_bytes(int batch, int total, int vocab) {
-  const size_t sc = scan_chunks<uint32_t>(vocab), pc = pick_chunks(vocab);  // fp32: the more
+  const size_t sc = scan_chunks<uint32_t>(vocab), pc = pick_chunks(vocab, kFew);  // the more of them
   return align16((size_t)(total + batch) * sc * sizeof(float2)) +
          align16((size_t)(total + batch) * sizeof(float)) + align16((size_t)total) +
          align16((size_t)batch * sizeof(Draw)) + (size_t)batch * 2 * pc * sizeof(Part) +
@@ -644,7 +669,7 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   p.target_prob = a.target_prob;
   p.err = a.err;
   p.arrived = a.arrived;
-  const size_t sc = scan_chunks<uint32_t>(a.vocab), pc = pick_chunks(a.vocab);
+  const size_t sc = scan_chunks<uint32_t>(a.vocab), pc = pick_chunks(a.vocab, kFew);
   uint8_t* s = static_cast<uint8_t*>(a.scratch);
   p.scan = reinterpret_cast<float2*>(s);
   s += align16((size_t)(a.total + a.batch) * sc * sizeof(float2));

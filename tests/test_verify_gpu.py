@@ -199,3 +199,13 @@ def test_verify_on_another_stream():
     o = dd.verify_draft(**dev, temperature=tau, draft_temperature=tau_d, stream=side)
     side.synchronize()
     assert all(torch.equal(o[x].cpu(), want[x]) for x in want)
+
+
+@pytest.mark.parametrize("k,V", [
+    ((9,), 262144), ((2, 3, 0), 99001),                   # few chunks of the drawn rows
+    ((1, 2, 0, 3, 2), 65537), ((1,) * 75, 4099),          # many
+])
+def test_verify_draws_over_few_and_many_chunks(k, V):
+    for seed in range(2):
+        c, tau, tau_d = _case(k, V, torch.bfloat16, 7 * V + seed, 0.7, 1.0, 0.9)
+        _check(c, tau, tau_d)
