@@ -28,9 +28,11 @@
 // E4M3 cache: a code is exact in fp16, and the products run on the codes
 // themselves, in fp16.  The key's scale 2^ek multiplies its scores.  The
 // value's scale 2^ev enters the exponent: with x the log2-domain score, the
-// weights are w = 2^(x + ev - m) with m the running maximum of x + ev, so
-// that O = sum w code is always within fp16's range, and the softmax's sum is
-// that of 2^(x - m) = w 2^-ev.  The bf16 query is scaled by a power of two per
+// weights are w = 2^(x + ev - n) with n the running maximum of x + ev, so
+// that O = sum w code is always within fp16's range.  The softmax's sum is that
+// of 2^(x - m), m the running maximum of x, with exponentials of its own: x
+// and x + ev can lie 240 octaves apart, more than fp32 holds beside a sum.
+// The bf16 query is scaled by a power of two per
 // row that puts its largest magnitude in [2^14, 2^15); only what lies 2^28
 // below it loses bits.
 //
@@ -66,7 +68,7 @@ struct Few {
   static constexpr int kMostWhole = kF8 ? 6 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kLd = D + 4;  // floats per row of the merge area
-  static constexpr int kSmem = kWarps * kRows * (kLd + 2) * 4;
+  static constexpr int kSmem = kWarps * kRows * (kLd + (kF8 ? 3 : 2)) * 4;
 };
 
 __device__ __forceinline__ uint4 ld16(const void* p) {
@@ -118,11 +120,12 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
   constexpr int kKS = kF8 ? 4 : 2;        // products per block
   constexpr int kMT = D / 16;             // products per 16 keys of V
   constexpr int kVB = kRow / 8;           // bytes of a V row per lane
-  extern __shared__ float area[];         // merge area: O, then m and l
+  extern __shared__ float area[];         // merge area: O, then m and l, and n (8-bit cache)
   __shared__ Share share;
   __shared__ int64_t warp_sums[F::kWarps];
   float* area_m = area + F::kWarps * F::kRows * F::kLd;
   float* area_l = area_m + F::kWarps * F::kRows;
+  float* area_n = area_l + F::kWarps * F::kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   pdl_wait();
@@ -183,10 +186,10 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
     }
     // ---- the keys of this warp: chunks of 16, every kWarps-th of the segment
     float o[NT][kMT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], n[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -1e30f;
+      m[nt][0] = m[nt][1] = n[nt][0] = n[nt][1] = -1e30f;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int t = 0; t < kMT; ++t)
@@ -296,14 +299,13 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
           }
         }
       }
-      // 2^ek, ev and 2^-ev of keys g, g + 8
-      float fk[2], ev[2], fv[2];
+      // 2^ek and ev of keys g, g + 8
+      float fk[2], ev[2];
       if constexpr (kF8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           fk[h] = __uint_as_float(ks[h] << 23);
           ev[h] = __uint_as_float(0x4b000000u + vs[h]) - (8388608.f + 127.f);  // 2^23 + byte
-          fv[h] = __uint_as_float((254u - vs[h]) << 23);
         }
       }
       if (more) load_k(place);  // in flight over the rest of this chunk
@@ -315,25 +317,31 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int h = e >> 1, u = e & 1;
-          const float x = kF8 ? fmaf(s[nt][e], fk[h] * scale[nt][u], ev[h]) : s[nt][e] * scale[nt][u];
+          const float x = s[nt][e] * (kF8 ? fk[h] * scale[nt][u] : scale[nt][u]);
           s[nt][e] = i * 16 + h * 8 + g < lim[nt][u] ? x : -INFINITY;
           grow |= s[nt][e] > m[nt][u] + kLazy;
+          if constexpr (kF8) grow |= s[nt][e] + ev[h] > n[nt][u] + kLazy;
         }
       }
-      // the reference moves only when a score passes it by a margin
+      // the references move only when a score passes one by a margin
       if (__any_sync(0xffffffffu, grow)) {
+        auto move = [&](float& ref, float a, float b) {  // to the keys' maximum; the factor
+          a = fmaxf(a, b);
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+          a = fmaxf(ref, a);
+          const float f = ex2_approx(ref - a);
+          ref = a;
+          return f;
+        };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            float mn = fmaxf(s[nt][u], s[nt][2 + u]);
-            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 4));
-            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
-            mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
-            mn = fmaxf(m[nt][u], mn);
-            const float al = ex2_approx(m[nt][u] - mn);
-            m[nt][u] = mn;
+            float al = move(m[nt][u], s[nt][u], s[nt][2 + u]);
             l[nt][u] *= al;
+            if constexpr (kF8) al = move(n[nt][u], s[nt][u] + ev[0], s[nt][2 + u] + ev[1]);
 #pragma unroll
             for (int t = 0; t < kMT; ++t) {
               o[nt][t][u] *= al;
@@ -347,7 +355,8 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           w[e] = ex2_approx(s[nt][e] - m[nt][e & 1]);
-          l[nt][e & 1] = kF8 ? fmaf(w[e], fv[e >> 1], l[nt][e & 1]) : l[nt][e & 1] + w[e];
+          l[nt][e & 1] += w[e];
+          if constexpr (kF8) w[e] = ex2_approx(s[nt][e] + (ev[e >> 1] - n[nt][e & 1]));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -402,6 +411,7 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
         if (g == 0) {
           area_m[r] = m[nt][u];
           area_l[r] = v;
+          if constexpr (kF8) area_n[r] = n[nt][u];
         }
 #pragma unroll
         for (int t = 0; t < kMT; ++t)
@@ -412,14 +422,18 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
     // ---- one warp per query row, D / 32 columns per lane
     constexpr int kC = D / 32;
     for (int r = warp; r < min(rows, F::kRows); r += F::kWarps) {
-      float top = -1e30f;
+      float top = -1e30f, ntop = -1e30f;
 #pragma unroll
-      for (int w = 0; w < F::kWarps; ++w) top = fmaxf(top, area_m[w * F::kRows + r]);
+      for (int w = 0; w < F::kWarps; ++w) {
+        top = fmaxf(top, area_m[w * F::kRows + r]);
+        if constexpr (kF8) ntop = fmaxf(ntop, area_n[w * F::kRows + r]);
+      }
       float sum = 0.f, acc[kC] = {};
 #pragma unroll
       for (int w = 0; w < F::kWarps; ++w) {
-        const float f = ex2_approx(area_m[w * F::kRows + r] - top);
+        float f = ex2_approx(area_m[w * F::kRows + r] - top);
         sum = fmaf(f, area_l[w * F::kRows + r], sum);
+        if constexpr (kF8) f = ex2_approx(area_n[w * F::kRows + r] - ntop);
         const float* src = area + (w * F::kRows + r) * F::kLd + lane * kC;
 #pragma unroll
         for (int e = 0; e < kC; ++e) acc[e] = fmaf(f, src[e], acc[e]);
@@ -428,6 +442,11 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
       const float lse = sum > 0.f ? top + __log2f(sum) : -INFINITY;
 #pragma unroll
       for (int e = 0; e < kC; ++e) acc[e] *= inv;
+      if constexpr (kF8) {  // O is in units of 2^(n - m), which may lie near either end of fp32
+        const float half = ex2_approx(0.5f * (ntop - top));
+#pragma unroll
+        for (int e = 0; e < kC; ++e) acc[e] = acc[e] * half * half;
+      }
       if (whole) {
         const int tok = div_G(p, r);
         const int64_t at = (int64_t)(sg.r.q0 + tok) * p.Hq + sg.g * p.G + r - tok * p.G;
