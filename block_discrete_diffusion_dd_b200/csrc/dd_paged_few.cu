@@ -28,11 +28,16 @@
 // E4M3 cache: a code is exact in fp16, and the products run on the codes
 // themselves, in fp16.  The key's scale 2^ek multiplies its scores.  The
 // value's scale 2^ev enters the exponent: with x the log2-domain score, the
-// weights are w = 2^(x + ev - n) with n the running maximum of x + ev, so
-// that O = sum w code is always within fp16's range.  The softmax's sum is that
-// of 2^(x - m), m the running maximum of x, with exponentials of its own: x
-// and x + ev can lie 240 octaves apart, more than fp32 holds beside a sum.
-// The bf16 query is scaled by a power of two per
+// weights are w = 2^(x + ev - n) in O = sum w code, with n a reference that
+// follows the maximum of x + ev over the keys whose V is not zero (a row of
+// zeros has the scale 2^0, often far above its neighbours', and adds nothing).
+// n lies 6 below the maximum when it moves and moves when a weight would pass
+// 2^15, so that a weight keeps fp16's 11 bits down to 2^-20 of the largest; what
+// a smaller one loses, 2^-25 of its codes at most, is under 2^-30 of what the
+// largest adds (as the cache is written, a row's largest code is above 224).
+// The softmax's sum is that of 2^(x - m), m the running maximum of x, with
+// exponentials of its own: x and x + ev can lie 240 octaves apart, more than
+// fp32 holds beside a sum.  The bf16 query is scaled by a power of two per
 // row that puts its largest magnitude in [2^14, 2^15); only what lies 2^28
 // below it loses bits.
 //
@@ -51,6 +56,9 @@ namespace {
 constexpr int kFixed = 2;  // an item's overhead in key tiles
 constexpr int kMinShare = 4;
 constexpr float kLazy = 8.0f;
+// E4M3 cache: log2 of a weight at the maximum when its reference moves, and of
+// the largest that a weight may get
+constexpr float kWeight = 6.0f, kMostWeight = 15.0f;
 
 // Warps per CTA and CTAs per SM by what a lane has to keep: 16 keys of data
 // (32 registers for 8-bit, 64 for bf16, at D = 128), the output (D / 4 per 8
@@ -320,17 +328,30 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
           const float x = s[nt][e] * (kF8 ? fk[h] * scale[nt][u] : scale[nt][u]);
           s[nt][e] = i * 16 + h * 8 + g < lim[nt][u] ? x : -INFINITY;
           grow |= s[nt][e] > m[nt][u] + kLazy;
-          if constexpr (kF8) grow |= s[nt][e] + ev[h] > n[nt][u] + kLazy;
+          if constexpr (kF8) grow |= s[nt][e] + ev[h] > n[nt][u] + kMostWeight;
         }
       }
       // the references move only when a score passes one by a margin
       if (__any_sync(0xffffffffu, grow)) {
-        auto move = [&](float& ref, float a, float b) {  // to the keys' maximum; the factor
+        if constexpr (kF8) {  // keys whose V is zero: weight 0
+          uint32_t some = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4& q = vd[u][0];
+            if ((q.x | q.y | q.z | q.w) & 0x7f7f7f7fu) some |= 1u << (2 * c + (u & 1) + 4 * (u & 2));
+          }
+          some = __reduce_or_sync(0xffffffffu, some);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (!(some >> (g + 8 * h) & 1u)) ev[h] = -INFINITY;
+        }
+        // to the keys' maximum, less `low`; returns the factor
+        auto move = [&](float& ref, float a, float b, float low) {
           a = fmaxf(a, b);
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-          a = fmaxf(ref, a);
+          a = fmaxf(ref, a - low);
           const float f = ex2_approx(ref - a);
           ref = a;
           return f;
@@ -339,9 +360,10 @@ __global__ void __launch_bounds__(Few<D, kF8, NT>::kThreads, Few<D, kF8, NT>::kB
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            float al = move(m[nt][u], s[nt][u], s[nt][2 + u]);
+            float al = move(m[nt][u], s[nt][u], s[nt][2 + u], 0.f);
             l[nt][u] *= al;
-            if constexpr (kF8) al = move(n[nt][u], s[nt][u] + ev[0], s[nt][2 + u] + ev[1]);
+            if constexpr (kF8)
+              al = move(n[nt][u], s[nt][u] + ev[0], s[nt][2 + u] + ev[1], kWeight);
 #pragma unroll
             for (int t = 0; t < kMT; ++t) {
               o[nt][t][u] *= al;
