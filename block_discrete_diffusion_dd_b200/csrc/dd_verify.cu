@@ -217,7 +217,9 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   };
-  // each warp has a reference of its own, which follows its maximum
+  // each warp has a reference of its own, which follows its maximum; rounded
+  // up, so that no exponent is above 0: where logits are large (a warp of
+  // masked entries, -1e10 say) half a step of their product with c is hundreds
   const float c = (float)p.c;
   const float2 c2 = make_float2(c, c);
   float ref = safe_max(-INFINITY) * c;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) v[i] = next[i];
     if (ch + 1 < per) load(chunk0 + ch + 1, next);
-    const float top = fmaxf(ref, warp_max(blocks_max<T>(v)) * c);
+    const float top = fmaxf(ref, __fmul_ru(warp_max(blocks_max<T>(v)), c));
     const float f = ex2_approx(ref - top);
     s2 = __fmul2_rn(s2, make_float2(f, f));
     ref = top;

@@ -1,0 +1,26 @@
+"""GPU tests of dd_verify_draft where logits are unusual or decisions close,
+against a plain 64-bit form (paged_ref.py): decisions and draws are equal,
+target_prob is within the tolerance of test_verify_gpu.py."""
+import pytest
+import torch
+
+from test_verify_gpu import _case, _check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("mask", [-1e9, -1e10, -3e10, -1e12, -1e15, -1e20, -1e29, -3e38])
+def test_verify_large_finite_masks(dtype, mask):
+    # most of the vocabulary masked by a large finite value: whole chunks of it
+    V = 50000
+    c, tau, tau_d = _case((5, 3), V, dtype, 31, noise=0.3, tau=0.9, tau_d=0.9)
+    keep = 7000
+    for z in ("target_logits", "draft_logits"):
+        c[z][:, keep:] = mask
+    q = torch.softmax(c["draft_logits"].double() / tau_d, -1)
+    tok = torch.multinomial(q, 1, generator=torch.Generator().manual_seed(4))
+    c["draft_tokens"] = tok[:, 0].to(torch.int32)
+    c["draft_conf"] = q.gather(1, tok)[:, 0].float()
+    o = _check(c, tau, tau_d)
+    assert o["accepted"].sum() > 0 and (o["tokens"] < keep).all()
