@@ -40,6 +40,7 @@
 // cycles) and norm and pick 25; one sequence with eight drafted tokens 17.9
 // us, nearly all of it the chain of the three kernels.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "dd_paged.cuh"
@@ -49,10 +50,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlocks = 4;               // 16-byte blocks of a thread of the scan
+constexpr int kScanBlocks = 5;           // CTAs of the scan per SM (48 registers)
 // entries of a thread of norm and pick (kPer): 8, or 4 where that makes few
 // chunks (launch_verify_t)
 constexpr int kFew = 4, kMany = 8;
 constexpr double kNear = 1e-5;
+// Scaled logits up to which a row's fp32 reference is good enough: a step of
+// 2^28 is 32, which fp32 exponentials have room for.  Rows beyond it (a mask of
+// the type's lowest value that leaves nothing, say) are summed in 64 bits, by a
+// warp each.
+constexpr float kWide = 268435456.f;
 
 // What `norm` hands on about sequence b's draw.
 struct Draw {
@@ -136,7 +143,7 @@ __device__ __forceinline__ Pair block_sum2(double x, double y, Pair* sm) {
 
 // A maximum that exponents may be taken against: rows (chunks) of -inf only
 // get a finite one, against which every term is 0.
-__device__ __forceinline__ float safe_max(float m) { return fmaxf(m, -1.0e30f); }
+__device__ __forceinline__ float safe_max(float m) { return fmaxf(m, -FLT_MAX); }
 
 // Entries of a 16-byte block as floats.
 template <typename T>
@@ -173,12 +180,26 @@ __device__ __forceinline__ float blocks_max(const uint4 (&v)[kBlocks]) {
   }
 }
 
+// p of the entry x1 of one row in 64 bits throughout (one warp; not inlined, so
+// that the scan stays at 48 registers: at 62 a call takes 1.5 to 2.5 us more).
+template <typename T>
+__device__ __noinline__ double wide_prob(const T* x, int vocab, double c, float x1) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY;
+  for (int v = lane; v < vocab; v += 32) m = fmaxf(m, logit(x, v));
+  m = safe_max(warp_max(m));
+  double s = 0;
+  for (int v = lane; v < vocab; v += 32) s += exp2(((double)logit(x, v) - (double)m) * c);
+  s = warp_sum(s);
+  return s > 0 ? exp2(((double)x1 - (double)m) * c) / s : 0;
+}
+
 // A row is read in aligned 16-byte blocks, whatever its start; entries of the
 // first and the last block that are not the row's count as -inf.  A CTA takes
 // `per` chunks of kThreads * kBlocks blocks of one row, the next one's blocks
 // in flight while the exponentials of one are summed.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kScanBlocks)
     verify_scan_kernel(const VerifyParams p, int segs, int per) {
   constexpr int kE = 16 / sizeof(T);
   __shared__ float2 sm[kThreads / 32];
@@ -222,7 +243,7 @@ __global__ void __launch_bounds__(kThreads)
   // masked entries, -1e10 say) half a step of their product with c is hundreds
   const float c = (float)p.c;
   const float2 c2 = make_float2(c, c);
-  float ref = safe_max(-INFINITY) * c;
+  float ref = safe_max(safe_max(-INFINITY) * c);
   float2 s2 = make_float2(0.f, 0.f);
   uint4 next[kBlocks];
   load(chunk0, next);
@@ -298,13 +319,17 @@ __global__ void __launch_bounds__(kThreads)
       sum += (double)v.y * exp2f(v.x - top);
     }
     sum = warp_sum(sum);
+    const bool wide = !(fabsf(top) < kWide);
+    double pr = 0;
+    if (wide && drafted && in)
+      pr = wide_prob(static_cast<const T*>(p.target) + r * p.target_stride, p.vocab, p.c, x1);
     if (lane == 0) {
       p.ref[r] = top;
       if (drafted) {
         if (!in) atomicOr(p.err, kDevErrBounds);
-        const double pr = in && sum > 0 ? exp2((double)x1 * (double)c - (double)top) / sum : 0;
+        if (!wide && in && sum > 0) pr = exp2((double)x1 * (double)c - (double)top) / sum;
         p.target_prob[t] = (float)pr;
-        p.state[t] = pr == 0 ? 1 : fabs(bar - pr) <= kNear * pr ? 2 : bar < pr ? 0 : 1;
+        p.state[t] = pr == 0 ? 1 : !wide && fabs(bar - pr) <= kNear * pr ? 2 : bar < pr ? 0 : 1;
       }
     }
   }

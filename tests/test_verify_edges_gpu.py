@@ -24,3 +24,21 @@ def test_verify_large_finite_masks(dtype, mask):
     c["draft_conf"] = q.gather(1, tok)[:, 0].float()
     o = _check(c, tau, tau_d)
     assert o["accepted"].sum() > 0 and (o["tokens"] < keep).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_verify_rows_of_extreme_logits(dtype):
+    # rows of the type's lowest value (a mask that leaves nothing: uniform), or
+    # of magnitudes whose scaled value is far beyond the fp32 exponents' reach
+    low, V = torch.finfo(dtype).min, 3001
+    for seed, fill in enumerate((low, -1e35, -4e30, 1e9, -2e9, 3e12, 1e38, 3e38)):
+        c, tau, tau_d = _case((2, 1), V, dtype, 40 + seed, noise=0.3)
+        c["target_logits"][:] = fill
+        c["draft_logits"][:] = low
+        c["draft_conf"][:] = 1 / V
+        c["u_accept"] = torch.tensor([0.999, 0.5, 0.25])
+        for r in range(5):  # a few lower entries
+            c["target_logits"][r, r::7] = low if fill > 0 else 1.5 * fill if fill > -1e38 else fill
+        c["draft_tokens"] = torch.tensor([1, 3, 10], dtype=torch.int32)
+        for t in (0.25, 1.0, 2.0):
+            _check(c, t, tau_d)
