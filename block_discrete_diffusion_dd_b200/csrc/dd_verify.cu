@@ -17,10 +17,15 @@
 //           per entry: 23 us of MUFU time against 30 us of HBM time for 390
 //           bf16 rows of 262,144).  The chunk that finishes a row merges its
 //           chunks, forms p(x_i) and tests it.  A test within kNear of equality
-//           is left open: an exponent x c - r is off by at most 2^-24 of itself
-//           and c by 2^-25 of itself, which moves p by less than 1e-6 for
-//           scores within 30 of each other and by less than kNear for the
-//           smallest p that u_i conf_i (fp32 factors) can equal.
+//           is left open.  kNear covers what p(x_i) may be off by: c is within
+//           2^-24 of itself, which moves log2 p(x_i) by 2^-24 |log2 p(x_i) + H|,
+//           H the row's entropy in bits, hence p by 1.2e-5 at 2^-298, the least
+//           that u_i conf_i (fp32 factors) can be; a lane adds up to 128 terms
+//           (7.6e-6), its warp and the row's chunks 14 more (0.8e-6); a sum is
+//           scaled up to eight times (2.4e-6); exponents are rounded by 2^-24 of
+//           themselves, twice (5e-6 where they count: H <= 30, a reference up to
+//           32 above the maximum), exponentials by 2^-22, three times (0.7e-6).
+//           In all 3e-5.
 //   norm    finds the first refusal, repeating open tests with 64-bit sums over
 //           their rows, so that the decision is the one exact arithmetic takes;
 //           then, for the one row the next token is drawn at, the 64-bit sums of
@@ -54,7 +59,7 @@ constexpr int kScanBlocks = 5;           // CTAs of the scan per SM (48 register
 // entries of a thread of norm and pick (kPer): 8, or 4 where that makes few
 // chunks (launch_verify_t)
 constexpr int kFew = 4, kMany = 8;
-constexpr double kNear = 1e-5;
+constexpr double kNear = 4e-5;
 // Scaled logits up to which a row's fp32 reference is good enough: a step of
 // 2^28 is 32, which fp32 exponentials have room for.  Rows beyond it (a mask of
 // the type's lowest value that leaves nothing, say) are summed in 64 bits, by a

@@ -1,10 +1,13 @@
 """GPU tests of dd_verify_draft where logits are unusual or decisions close,
 against a plain 64-bit form (paged_ref.py): decisions and draws are equal,
 target_prob is within the tolerance of test_verify_gpu.py."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
-from test_verify_gpu import _case, _check
+from test_verify_gpu import _case, _check, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +45,31 @@ def test_verify_rows_of_extreme_logits(dtype):
         c["draft_tokens"] = torch.tensor([1, 3, 10], dtype=torch.int32)
         for t in (0.25, 1.0, 2.0):
             _check(c, t, tau_d)
+
+
+def _near_tie(tau, bar_u, bar_conf, off):
+    """Three logits whose p(1) lies `off` (relative) above bar_u * bar_conf."""
+    c = math.log2(math.e) / float(np.float32(tau))
+    bar = math.log2(bar_u) + math.log2(bar_conf)
+    x1 = np.float32((bar + 0.5) / c)
+    Z = 2.0 ** (float(x1) * c - bar) / (1 + off)
+    x2 = np.float32(math.log2(Z - 1) / c)
+    z = torch.tensor([[0.0, x1, x2], [0.0, 0.0, 0.0]])
+    p = 2.0 ** (float(x1) * c - bar) / (1 + 2.0 ** (float(x2) * c))  # over the bar
+    return z, p - 1
+
+
+# constants log2(e) / tau that fp32 holds worst (one too large, one too small), and 1.3
+@pytest.mark.parametrize("tau", [1.4424631595611572, 1.4425914287567139, 1.3])
+@pytest.mark.parametrize("off", [2e-6, -2e-6, 5e-7, -5e-7])
+def test_verify_decides_tiny_probabilities_exactly(tau, off):
+    # u conf at the smallest product of two fp32 numbers, p a hair from it
+    u, conf = 2.0 ** -149, 2.0 ** -149
+    z, got = _near_tie(tau, u, conf, off)
+    assert off * got > 0 and abs(got) > 1e-7
+    case = dict(target_logits=z, draft_logits=z[:1], draft_tokens=torch.tensor([1], dtype=torch.int32),
+                draft_conf=torch.tensor([conf]), cu_draft=torch.tensor([0, 1], dtype=torch.int32),
+                u_accept=torch.tensor([u]), u_sample=torch.tensor([0.5]))
+    assert case["draft_conf"].item() == conf
+    o = _run(case, float(np.float32(tau)), 1.0)
+    assert o["accepted"].tolist() == [1 if off > 0 else 0]
