@@ -29,12 +29,15 @@
 // codes of every row); 81,986 tokens of a bf16 cache read in 104 us, the rate
 // of a copy; 4,096 tokens of an E4M3 cache read in 5.8 us; one token of 32
 // sequences appended in 2.7 us.
+#include <climits>
+
 #include "dd_paged.cuh"
 
 namespace dd {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocks = 4;  // CTAs per SM (64 registers)
 
 // Largest |x| of the 8 bf16 values in v, as bf16 bits (which order like the
 // magnitudes they stand for; 0x7f80 and above are infinities and NaN).
@@ -111,20 +114,122 @@ struct Step {
   }
 };
 
-// Pool rows (head 0) of the CTA's tokens, -1 for those without a place.
-template <typename F>
-__device__ __forceinline__ void place_tokens(int64_t* rows, int first, int count, int total, F&& of) {
-  for (int k = threadIdx.x; k < count; k += kThreads)
-    rows[k] = first + k < total ? of(first + k) : -1;
+// Pool rows (head 0) of the CTA's tokens, -1 for those without a place: row(b,
+// end) is sequence b where the possible ones before it end at `end`, of(t, b, c)
+// the place of its packed row t, and `most` the packed rows there may be.
+// Returns whether the offsets are in order, which other warps find beside the
+// search that trusts they are; if not, place_in_turn finds the places.  (The
+// first CTA checks rows without tokens of this call too.)
+template <typename R, typename F>
+__device__ __forceinline__ bool place_tokens(int64_t* rows, int first, int count,
+                                             const PagedBatch& p, int most, R&& row, F&& of) {
+  bool order = true;
+  for (int b = (int)((threadIdx.x + kThreads - 32) % kThreads); b < p.batch; b += kThreads) {
+    order = offsets_fit(p.cu_new, b, most) && order;
+    if (blockIdx.x == 0) row(b, 0);
+  }
+  for (int k = threadIdx.x; k < count; k += kThreads) {
+    const int t = first + k;
+    const int b = t < p.total_new ? owner_row(p.cu_new, p.batch, t) : -1;
+    rows[k] = -1;
+    if (b < 0) continue;
+    const ChunkRow c = row(b, 0);
+    if (t >= c.q0 && t - c.q0 < c.n) rows[k] = of(t, b, c);
+  }
+  return __syncthreads_and(order);
+}
+template <typename R, typename F>
+__device__ __forceinline__ void place_in_turn(int64_t* rows, int first, int count,
+                                              const PagedBatch& p, R&& row, F&& of) {
+  for (int k = threadIdx.x; k < count; k += kThreads) {
+    const int t = first + k;
+    rows[k] = -1;
+    ChunkRow c{0, 0, 0};
+    for (int b = 0; b < p.batch && t < p.total_new; ++b) {
+      c = row(b, c.q0 + c.n);
+      if (t >= c.q0 && t - c.q0 < c.n) rows[k] = of(t, b, c);
+    }
+  }
   __syncthreads();
 }
 
+// The place of packed row t of sequence b.
+__device__ __forceinline__ int64_t append_row(const PagedBatch& p, int t, int b, const ChunkRow& c,
+                                              uint32_t* err) {
+  const int pos = c.len - c.n + (t - c.q0);
+  return pos >= 0 ? pool_row(p, b, pos, err) : -1;
+}
+
+struct Append {
+  const uint16_t *k_new, *v_new;
+  int64_t k_stride, v_stride;
+  void *k_pool, *v_pool;
+  uint8_t *k_scale, *v_scale;
+  uint32_t* err;
+};
+
+// This lane's 16 bytes of the unit (token, hv), and their way into the pool,
+// where the token's head 0 has the row `row` (ok: it has one).  The lanes of a
+// warp call the second together.
+template <int D>
+__device__ __forceinline__ uint4 load_unit(const Append& a, int heads, int tok, int hv, int l) {
+  const uint16_t* src = hv < heads ? a.k_new + tok * a.k_stride + hv * D
+                                   : a.v_new + tok * a.v_stride + (hv - heads) * D;
+  return __ldg(reinterpret_cast<const uint4*>(src) + l);
+}
+template <int D, bool kF8>
+__device__ __forceinline__ void store_unit(const PagedBatch& p, const Append& a, int64_t row,
+                                           bool ok, int hv, int l, uint4 v) {
+  constexpr int kLanes = D / 8;
+  const int H = p.heads_kv;
+  const bool is_v = hv >= H;
+  row += (int64_t)(is_v ? hv - H : hv) << p.page_shift;
+  if constexpr (!kF8) {
+    if (ok) reinterpret_cast<uint4*>(is_v ? a.v_pool : a.k_pool)[row * kLanes + l] = v;
+  } else {
+    uint32_t s = scale_byte(row_max<kLanes>(amax_bits(v)));
+    uint2 c;
+    // one comparison covers non-finite values and the largest exponent
+    if (!__any_sync(0xffffffffu, s >= 247u)) {
+      const float inv = pow2f(127 - (int)s);
+      c.x = quant4(v.x, v.y, inv);
+      c.y = quant4(v.z, v.w, inv);
+    } else {
+      s = scale_byte(row_max<kLanes>(amax_finite_bits(v)));
+      const float inv = pow2f(127 - (int)s), top = s == 247u ? 240.f : 448.f;
+      c.x = quant4_rare(v.x, v.y, inv, top);
+      c.y = quant4_rare(v.z, v.w, inv, top);
+    }
+    if (ok) {
+      reinterpret_cast<uint2*>(is_v ? a.v_pool : a.k_pool)[row * kLanes + l] = c;
+      if (l == 0) (is_v ? a.v_scale : a.k_scale)[row] = (uint8_t)s;
+    }
+  }
+}
+
+// A CTA's units where the offsets are not in order.
 template <int D, bool kF8, int N>
-__global__ void __launch_bounds__(kThreads)
-    cache_append_kernel(const PagedBatch p, const uint16_t* __restrict__ k_new,
-                        const uint16_t* __restrict__ v_new, int64_t k_stride, int64_t v_stride,
-                        void* k_pool, void* v_pool, uint8_t* k_scale, uint8_t* v_scale,
-                        uint32_t* err) {
+__device__ __noinline__ void append_in_turn(const PagedBatch& p, const Append& a, int64_t* rows) {
+  using U = Units<D, N>;
+  const int H = p.heads_kv, l = threadIdx.x % U::kLanes;
+  const int first = blockIdx.x * U::kPer / (2 * H);
+  place_in_turn(
+      rows, first, min(U::kTokens, (U::kPer - 1) / (2 * H) + 2), p,
+      [&](int b, int end) { return chunk_row(p, b, end, a.err); },
+      [&](int t, int b, const ChunkRow& c) { return append_row(p, t, b, c, a.err); });
+  for (int i = 0; i < N; ++i) {
+    const int u = blockIdx.x * U::kPer + threadIdx.x / U::kLanes + i * U::kGroups;
+    const int tok = u / (2 * H), hv = u - tok * 2 * H;
+    const bool in = tok < p.total_new;
+    const uint4 v = in ? load_unit<D>(a, H, tok, hv, l) : make_uint4(0u, 0u, 0u, 0u);
+    const int64_t row = in ? rows[tok - first] : -1;
+    store_unit<D, kF8>(p, a, row, row >= 0, hv, l, v);
+  }
+}
+
+template <int D, bool kF8, int N>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    cache_append_kernel(const __grid_constant__ PagedBatch p, const __grid_constant__ Append a) {
   using U = Units<D, N>;
   __shared__ int64_t rows[U::kTokens];
   pdl_wait();
@@ -141,53 +246,22 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < N; ++i) {
     if (i > 0) step(tok[i - 1], hv[i - 1], tok[i], hv[i]);
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tok[i] < p.total_new) {
-      const uint16_t* src = hv[i] < H ? k_new + tok[i] * k_stride + hv[i] * D
-                                      : v_new + tok[i] * v_stride + (hv[i] - H) * D;
-      v[i] = __ldg(reinterpret_cast<const uint4*>(src) + l);
-    }
+    if (tok[i] < p.total_new) v[i] = load_unit<D>(a, H, tok[i], hv[i], l);
   }
-  place_tokens(rows, first, min(U::kTokens, (U::kPer - 1) / (2 * H) + 2), p.total_new, [&](int t) {
-    const int b = owner_row(p.cu_new, p.batch, t);
-    if (b < 0) return (int64_t)-1;
-    const ChunkRow c = chunk_row(p, b, err);
-    const int pos = c.len - c.n + (t - c.q0);
-    // (a row taken as empty has no position for its tokens)
-    return t - c.q0 < c.n && pos >= 0 ? pool_row(p, b, pos, err) : (int64_t)-1;
-  });
+  const bool order = place_tokens(
+      rows, first, min(U::kTokens, (U::kPer - 1) / (2 * H) + 2), p, p.total_new,
+      [&](int b, int end) { return chunk_row(p, b, end, a.err); },
+      [&](int t, int b, const ChunkRow& c) { return append_row(p, t, b, c, a.err); });
+  if (!order) return append_in_turn<D, kF8, N>(p, a, rows);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const bool is_v = hv[i] >= H;
-    int64_t row = rows[min(tok[i] - first, U::kTokens - 1)];
-    const bool ok = row >= 0 && tok[i] < p.total_new;
-    row += (int64_t)(is_v ? hv[i] - H : hv[i]) << p.page_shift;
-    if constexpr (!kF8) {
-      if (ok) reinterpret_cast<uint4*>(is_v ? v_pool : k_pool)[row * U::kLanes + l] = v[i];
-    } else {
-      const uint32_t a = row_max<U::kLanes>(amax_bits(v[i]));
-      uint32_t s = scale_byte(a);
-      uint2 c;
-      // one comparison covers non-finite values and the largest exponent
-      if (!__any_sync(0xffffffffu, s >= 247u)) {
-        const float inv = pow2f(127 - (int)s);
-        c.x = quant4(v[i].x, v[i].y, inv);
-        c.y = quant4(v[i].z, v[i].w, inv);
-      } else {
-        s = scale_byte(row_max<U::kLanes>(amax_finite_bits(v[i])));
-        const float inv = pow2f(127 - (int)s), top = s == 247u ? 240.f : 448.f;
-        c.x = quant4_rare(v[i].x, v[i].y, inv, top);
-        c.y = quant4_rare(v[i].z, v[i].w, inv, top);
-      }
-      if (ok) {
-        reinterpret_cast<uint2*>(is_v ? v_pool : k_pool)[row * U::kLanes + l] = c;
-        if (l == 0) (is_v ? v_scale : k_scale)[row] = (uint8_t)s;
-      }
-    }
+    const int64_t row = rows[min(tok[i] - first, U::kTokens - 1)];
+    store_unit<D, kF8>(p, a, row, row >= 0 && tok[i] < p.total_new, hv[i], l, v[i]);
   }
 }
 
 template <int D, bool kF8, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocks)
     cache_read_kernel(const PagedBatch p, const void* k_pool, const void* v_pool,
                       const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
                       uint4* __restrict__ k_out, uint4* __restrict__ v_out, uint32_t* err) {
@@ -198,16 +272,22 @@ __global__ void __launch_bounds__(kThreads)
   const int H = p.heads_kv, l = threadIdx.x % U::kLanes;
   const int u0 = blockIdx.x * U::kPer + threadIdx.x / U::kLanes;
   const int first = blockIdx.x * U::kPer / (2 * H);
-  place_tokens(rows, first, min(U::kTokens, (U::kPer - 1) / (2 * H) + 2), p.total_new, [&](int t) {
-    const int b = owner_row(p.cu_new, p.batch, t);
-    if (b < 0) return (int64_t)-1;
-    const int pos = t - __ldg(p.cu_new + b);
-    if (pos >= (p.max_pages << p.page_shift)) {
-      atomicOr(err, kDevErrBounds);
-      return (int64_t)-1;
-    }
-    return pool_row(p, b, pos, err);
-  });
+  // (a sequence may go on behind the rows that are asked for)
+  const int count = min(U::kTokens, (U::kPer - 1) / (2 * H) + 2);
+  auto row = [&](int b, int end) {
+    const int q0 = __ldg(p.cu_new + b), q1 = __ldg(p.cu_new + b + 1);
+    if (q0 >= end && q1 >= q0) return ChunkRow{q0, q1 - q0, q1 - q0};
+    atomicOr(err, kDevErrBounds);
+    return ChunkRow{end, 0, 0};
+  };
+  auto place = [&](int t, int b, const ChunkRow& c) {
+    const int pos = t - c.q0;
+    if (pos < (p.max_pages << p.page_shift)) return pool_row(p, b, pos, err);
+    atomicOr(err, kDevErrBounds);
+    return (int64_t)-1;
+  };
+  if (!place_tokens(rows, first, count, p, INT_MAX, row, place))
+    place_in_turn(rows, first, count, p, row, place);
   uint4 v[N];
   uint32_t sc[N];
   int64_t out[N];  // output row, -1: none; complemented for V
@@ -267,9 +347,9 @@ cudaError_t append_t(const CacheAppendArgs& a, int64_t units, cudaStream_t strea
   using U = Units<D, N>;
   cudaError_t e = launch_pdl(
       cache_append_kernel<D, kF8, N>, dim3((unsigned)((units + U::kPer - 1) / U::kPer)),
-      dim3(kThreads), 0, stream, a.p, static_cast<const uint16_t*>(a.k_new),
-      static_cast<const uint16_t*>(a.v_new), a.k_stride, a.v_stride, a.pool.k, a.pool.v,
-      a.pool.k_scale, a.pool.v_scale, a.err);
+      dim3(kThreads), 0, stream, a.p,
+      Append{static_cast<const uint16_t*>(a.k_new), static_cast<const uint16_t*>(a.v_new),
+             a.k_stride, a.v_stride, a.pool.k, a.pool.v, a.pool.k_scale, a.pool.v_scale, a.err});
   note_launch();
   return e;
 }

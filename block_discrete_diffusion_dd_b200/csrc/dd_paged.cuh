@@ -3,8 +3,12 @@
 //
 // Lengths, offsets and page ids live in device memory, where the host cannot
 // check them before a launch, so every kernel checks what it uses: a batch
-// row with impossible lengths is taken as empty, a page id outside the pool
-// is never followed, and both latch kDevErrBounds in the workspace header.
+// row with impossible lengths or offsets is taken as empty, a page id outside
+// the pool is never followed, and both latch kDevErrBounds in the workspace
+// header.  A row that starts before the end of an earlier possible one is
+// impossible too, so that a packed row has one owner at most.  Where every
+// row's offsets are possible by themselves they are in order, and the owner is
+// found by bisection; otherwise the rows are gone through one after the other.
 #pragma once
 
 #include "dd_device.cuh"
@@ -18,22 +22,31 @@ struct ChunkRow {
   int len;  // tokens in the cache, the new ones included
 };
 
-__device__ __forceinline__ ChunkRow chunk_row(const PagedBatch& p, int b, uint32_t* err) {
+// Whether the offsets of row b are possible by themselves, with `most` packed rows.
+__device__ __forceinline__ bool offsets_fit(const int32_t* cu, int b, int most) {
+  const int q0 = __ldg(cu + b), q1 = __ldg(cu + b + 1);
+  return q0 >= 0 && q1 >= q0 && q1 <= most;
+}
+
+// Row b, where the possible rows before it end at `end`; an impossible one has
+// no tokens and starts (and ends) there.
+__device__ __forceinline__ ChunkRow chunk_row(const PagedBatch& p, int b, int end, uint32_t* err) {
   ChunkRow r;
   r.q0 = __ldg(p.cu_new + b);
   const int q1 = __ldg(p.cu_new + b + 1);
   r.len = __ldg(p.kv_len + b);
-  r.n = q1 - r.q0;
-  if (r.q0 < 0 || q1 < r.q0 || q1 > p.total_new || r.n > p.max_new || r.len < 0 ||
+  if (r.q0 < end || q1 < r.q0 || q1 > p.total_new || q1 - r.q0 > p.max_new || r.len < 0 ||
       (int64_t)r.len > ((int64_t)p.max_pages << p.page_shift)) {
     atomicOr(err, kDevErrBounds);
-    r.q0 = r.n = r.len = 0;
+    return ChunkRow{end, 0, 0};
   }
+  r.n = q1 - r.q0;
   return r;
 }
 
-// The batch row that owns packed row t: the last b with cu[b] <= t (rows of
-// no tokens are passed over), or -1 when t lies at or past cu[batch].
+// The batch row that owns packed row t, offsets in order: the last b with
+// cu[b] <= t (rows of no tokens are passed over), or -1 when t lies at or past
+// cu[batch].  (Offsets that are not: some b with cu[b] <= t < cu[b + 1], or -1.)
 __device__ __forceinline__ int owner_row(const int32_t* cu, int batch, int t) {
   if (t >= __ldg(cu + batch) || t < __ldg(cu)) return -1;
   int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]

@@ -99,7 +99,7 @@ struct Walk {
   int groups;
 
   __device__ __forceinline__ void load(const Params& p) {
-    r = chunk_row(p.b, b, p.err);
+    r = chunk_row(p.b, b, r.q0 + r.n, p.err);
     groups = tile_groups<kRows>(r, p.G);
   }
   __device__ __forceinline__ bool next(const Params& p, Seg& s) {
@@ -188,6 +188,10 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool narrow = p.b.batch <= 32;  // one warp's work
   if (!narrow || warp == 0) {
+  bool order = true;  // every row's offsets are possible by themselves
+  for (int b = threadIdx.x; b < p.b.batch; b += kT)
+    order = offsets_fit(p.b.cu_new, b, p.b.total_new) && order;
+  order = narrow ? __all_sync(0xffffffffu, order) : __syncthreads_and(order);
   bool many = false;  // an item of more than kMost tiles (one barrier serves this too)
   int item = 0;       // units of an item of this thread's sequence
   // exclusive prefix of v over the block; *all gets the block's sum
@@ -222,7 +226,11 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
     const int b = b0 + threadIdx.x;
     w = 0;
     if (b < p.b.batch) {
-      r = chunk_row(p.b, b, p.err);
+      int end = 0;  // of the rows before
+      for (int a = order ? b : 0; a <= b; ++a) {
+        r = chunk_row(p.b, a, end, p.err);
+        end = r.q0 + r.n;
+      }
       w = row_weight<kRows, kFixed>(p, r);
       many = w > kMost + kFixed;
       item = (int)w;

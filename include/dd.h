@@ -531,8 +531,8 @@ typedef struct {
 /* A batch of sequences with new tokens, packed one after the other.
  *   batch       B >= 0 sequences
  *   max_pages   entries per row of page_table; max_pages * page_size <= 2^30
- *   total_new   rows of the packed new-token tensors; rows at or past
- *               cu_new[B] belong to no sequence, are not read, and their
+ *   total_new   rows of the packed new-token tensors; rows of no sequence
+ *               (those at or past cu_new[B], say) do not matter, and their
  *               outputs are left as they were
  *   max_new     no sequence has more new tokens than this
  *   page_table  int32 [B, max_pages]: position p of sequence b lies in page
@@ -545,7 +545,9 @@ typedef struct {
  *               kv_len[b] - n + i, n = cu_new[b+1] - cu_new[b]
  * A row is impossible, and taken as empty, unless 0 <= cu_new[b] <=
  * cu_new[b+1] <= total_new, n <= max_new and 0 <= kv_len[b] <=
- * max_pages * page_size.  kv_len[b] < n is possible: positions below 0 are
+ * max_pages * page_size, and unless it starts at or behind the end of every
+ * possible row before it (so a packed row has one owner at most); the other
+ * rows stand.  kv_len[b] < n is possible: positions below 0 are
  * not stored, and under a causal mask they see nothing. */
 typedef struct {
   int batch, max_pages, total_new, max_new;
@@ -577,11 +579,14 @@ DD_API dd_status dd_cache_append(const dd_paged_cache* cache, const dd_paged_bat
  * back, packed: the k_prefix, v_prefix and cu_prefix of dd_canvas_attn.  The
  * values are exact (an E4M3 code times a power of two is a bf16 number).
  *   page_table    int32 [batch, max_pages]
- *   cu_prefix     device int32 [batch + 1], 0 <= cu_prefix[0], non-decreasing
- *   total         rows of the outputs; rows outside [cu_prefix[0],
- *                 cu_prefix[batch]) are left as they were, and so are rows
- *                 whose position or page does not exist (which latch
- *                 DD_ERR_DEVICE_BOUNDS)
+ *   cu_prefix     device int32 [batch + 1]; a sequence is taken as empty
+ *                 (which latches DD_ERR_DEVICE_BOUNDS) unless 0 <=
+ *                 cu_prefix[b] <= cu_prefix[b+1] and it starts at or behind
+ *                 the end of every one before it that is not
+ *   total         rows of the outputs; rows of no sequence are left as they
+ *                 were, and so are rows whose position or page does not exist
+ *                 (which latch DD_ERR_DEVICE_BOUNDS); the prefixes may go on
+ *                 behind the last row
  *   k_out, v_out  bf16 [total, heads_kv, head_dim] */
 DD_API dd_status dd_cache_read(const dd_paged_cache* cache, int batch, int max_pages,
                                const int32_t* page_table, const int32_t* cu_prefix, int total,

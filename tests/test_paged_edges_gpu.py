@@ -87,3 +87,117 @@ def test_attention_e4m3_values_of_many_scales(new, past):
     cache, k64, v64 = _quantised_cache(_normal(shape, 11), torch.zeros(shape, dtype=torch.bfloat16))
     out = _check_attn(_normal((sum(new), 6, 128), 12), cache, k64, v64, pr)
     assert (out == 0).all()
+
+
+def _standing(cu, most):
+    """The rows that stand: possible by themselves and behind those before."""
+    end, rows = 0, []
+    for q0, q1 in zip(cu[:-1], cu[1:]):
+        rows.append(end <= q0 <= q1 <= most)
+        end = q1 if rows[-1] else end
+    return rows
+
+
+BIG = 2 ** 31 - 1
+OFFSETS = [
+    [0, 9, 5, 8],        # a row past the end: the last one stands all the same
+    [0, 8, 3, 6],        # a row inside the first one
+    [-4, 2, 5, 8],
+    [0, 3, -7, 8],
+    [0, BIG, -BIG - 1, 8],
+    [3, -BIG - 1, 5, 8],
+    [2, 2, 4, 8, 1, 8],
+    [8, 0, 8, 8],
+]
+FITTING = [[0, 3, 3, 8], [2, 4, 4, 7]]   # in order; packed rows of no sequence
+
+
+def _spoilt_batch(cu, unit, total, before=0, seed=3):
+    """A batch over the offsets, in units of `unit` tokens, behind `before`
+    rows of one token each: (problem of the rows that stand, cu, lens, batch)."""
+    def scaled(x):
+        return before + x * unit if abs(x) < 1000 else x
+
+    cu = list(range(before)) + [scaled(x) for x in cu]
+    total = before + total * unit
+    stands = _standing(cu, total)
+    new = [q1 - q0 if ok else 0 for q0, q1, ok in zip(cu[:-1], cu[1:], stands)]
+    lens = [7 + 3 * (b % 5) + n for b, n in enumerate(new)]
+    pr = ref.problem(new, [x - n for x, n in zip(lens, new)], 8, seed=seed)
+    pr.cu_new = torch.tensor(cu, dtype=torch.int32)
+    batch = dd.PagedBatch(pr.page_table.to(DEV), pr.cu_new.to(DEV), pr.kv_len.to(DEV), total)
+    return pr, total, all(stands), batch
+
+
+@pytest.mark.parametrize("unit,before", [(1, 0), (40, 0), (1, 290), (1, 1100)])
+@pytest.mark.parametrize("cu", OFFSETS + FITTING)
+def test_offsets_out_of_order_leave_the_standing_rows(cu, unit, before):
+    # append and attention agree on which rows those are, and touch no other's
+    H, D = 2, 64
+    pr, total, fine, batch = _spoilt_batch(cu, unit, 8, before)
+    cache, k64, v64 = _quantised_cache(*(_normal((pr.pages, H, 8, D), i) for i in (1, 2)))
+    cache = dd.PagedCache(k64.to(torch.bfloat16).to(DEV), v64.to(torch.bfloat16).to(DEV))
+    x = _normal((total, 2 * H, D), 4)
+    ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, total, 2 * H))
+    dd.cache_append(cache, batch, x[:, :H].to(DEV), x[:, H:].to(DEV), workspace=ws)
+    _latched(ws, not fine)
+    for b, n in enumerate(pr.new):
+        t0 = int(pr.cu_new[b])
+        for i in range(n):
+            pos = pr.lens[b] - n + i
+            at = int(pr.page_table[b, pos // 8]), slice(None), pos % 8
+            k64[at], v64[at] = x[t0 + i, :H].double(), x[t0 + i, H:].double()
+    assert torch.equal(cache.k.cpu().double(), k64) and torch.equal(cache.v.cpu().double(), v64)
+    q = _normal((total, 2 * H, D), 5)
+    for causal in (True, False):
+        out = torch.full((total, 2 * H, D), 7.0, dtype=torch.bfloat16, device=DEV)
+        dd.paged_attn(q.to(DEV), cache, batch, causal=causal, out=out, workspace=ws)
+        _latched(ws, not fine)
+        want, _, mag = ref.attention(q, k64, v64, pr, D ** -0.5, causal)
+        mine = torch.zeros(total, dtype=torch.bool)
+        for b, n in enumerate(pr.new):
+            mine[int(pr.cu_new[b]):int(pr.cu_new[b]) + n] |= n > 0
+        out = out.cpu().double()
+        err = (out - want).abs()[mine]
+        tol = (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * mag +
+               2.0 ** -11 * want.abs().amax(-1, keepdim=True))[mine]
+        assert (err <= tol).all()
+        assert (out[~mine] == 7).all()
+
+
+def _latched(ws, expected):
+    if not expected:
+        return dd.query_device_error(ws)
+    with pytest.raises(dd.DDError) as err:
+        dd.query_device_error(ws)
+    assert err.value.status == 6  # DD_ERR_DEVICE_BOUNDS
+    dd.query_device_error(ws)     # cleared by the query
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("cu", OFFSETS + FITTING)
+def test_prefixes_out_of_order_leave_the_standing_rows(cu, kind):
+    H, D, ps, total = 2, 64, 8, 10
+    stands = _standing(cu, BIG)
+    lens = [min(q1 - q0, total - q0) if ok and q0 < total else 0
+            for q0, q1, ok in zip(cu[:-1], cu[1:], stands)]
+    pr = ref.problem([0] * len(lens), lens, ps, seed=7)
+    k, v = (_normal((pr.pages, H, ps, D), i) for i in (1, 2))
+    cache, k64, v64 = _quantised_cache(k, v)
+    if kind == "bf16":
+        cache, k64, v64 = dd.PagedCache(k.to(DEV), v.to(DEV)), k.double(), v.double()
+    # (one page at least per row: what a search gone astray would look up)
+    width = max(pr.page_table.shape[1], 2)
+    table = torch.zeros((len(lens), width), dtype=torch.int32)
+    table[:, :pr.page_table.shape[1]] = pr.page_table.clamp(min=0)
+    kp, vp = (torch.full((total, H, D), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ws = dd.new_workspace(256)
+    dd.cache_read(cache, table.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV),
+                  k_out=kp, v_out=vp, workspace=ws)
+    _latched(ws, not all(stands))
+    for out, pool in ((kp, k64), (vp, v64)):
+        want = torch.full((total, H, D), 7.0, dtype=torch.float64)
+        for b, n in enumerate(lens):
+            if n:
+                want[cu[b]:cu[b] + n] = ref.sequence(pool, pr, b, n).transpose(0, 1)
+        assert torch.equal(out.double().cpu(), want)
