@@ -93,6 +93,7 @@ struct VerifyParams {
   float2* scan;       // [total + batch][segments]: reference, sum
   uint32_t* arrived;  // [kPagedCounters]: chunks done of the rows = i mod their number
   float* ref;         // [total + batch]: the rows' references
+  int* owner;         // [total + batch]: the sequence a row is of (if any is)
   uint8_t* state;     // [total]: 0 accepted, 1 refused, 2 near
   Draw* draw;         // [batch]
   Part* part;         // [batch][2][pick chunks]
@@ -218,6 +219,11 @@ __global__ void __launch_bounds__(kThreads, kScanBlocks)
   const int blocks = (p.vocab + skew + kE - 1) / kE;
   const bool whole = (p.vocab + skew) % kE == 0;  // the last block is all the row's
   const int chunk0 = seg * per;
+  // (asked before the logits are, needed after them)
+  bool order = true;
+#pragma unroll 1
+  for (int b = threadIdx.x; b < p.batch; b += kThreads)
+    order = offsets_fit(p.cu, b, p.total) && order;
   auto load = [&](int ch, uint4 (&v)[kBlocks]) {
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
@@ -292,18 +298,25 @@ __global__ void __launch_bounds__(kThreads, kScanBlocks)
     if (last) p.arrived[cls] = 0;  // for the next call
     __threadfence();
   }
-  __syncthreads();
+  order = __syncthreads_and(order);
   if (!last) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = cls + warp * (int)kPagedCounters; r < rows; r += kThreads / 32 * (int)kPagedCounters) {
-    // the sequence whose rows cu[b] + b .. cu[b + 1] + b hold r
-    int lo = 0, hi = p.batch;
+    // the sequence whose rows cu[b] + b .. cu[b + 1] + b hold r: by bisection,
+    // or in turn, of the rows of `cu` that stand, where they are not in order
+    int lo = order ? 0 : -1, hi = order ? p.batch : 0;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (__ldg(p.cu + mid) + mid <= r) lo = mid;
       else hi = mid;
     }
-    const int q0 = __ldg(p.cu + lo), q1 = __ldg(p.cu + lo + 1), t = r - lo;
+#pragma unroll 1
+    for (int a = 0, end = 0; !order && a < p.batch; ++a) {
+      if (!offsets_fit(p.cu, a, p.total) || __ldg(p.cu + a) < end) continue;
+      end = __ldg(p.cu + a + 1);
+      if (__ldg(p.cu + a) + a <= r) lo = a;
+    }
+    const int q0 = lo < 0 ? 0 : __ldg(p.cu + lo), q1 = lo < 0 ? 0 : __ldg(p.cu + lo + 1), t = r - lo;
     const bool drafted = q0 >= 0 && q1 <= p.total && t >= q0 && t < q1;
     int tok = -1;
     double bar = 0;
@@ -330,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, kScanBlocks)
       pr = wide_prob(static_cast<const T*>(p.target) + r * p.target_stride, p.vocab, p.c, x1);
     if (lane == 0) {
       p.ref[r] = top;
+      p.owner[r] = lo;
       if (drafted) {
         if (!in) atomicOr(p.err, kDevErrBounds);
         if (!wide && in && sum > 0) pr = exp2((double)x1 * (double)c - (double)top) / sum;
@@ -363,7 +377,8 @@ __device__ Draw find_draw(const VerifyParams& p, int b, bool mine) {
   __shared__ int first;
   Draw dr{0, -1, -1, 0};
   const int q0 = __ldg(p.cu + b), q1 = __ldg(p.cu + b + 1);
-  if (q0 < 0 || q1 < q0 || q1 > p.total) {
+  // possible by itself, and the scan gave it its target rows
+  if (q0 < 0 || q1 < q0 || q1 > p.total || p.owner[q0 + b] != b) {
     if (mine && threadIdx.x == 0) {
       atomicOr(p.err, kDevErrBounds);
       p.accepted[b] = 0;
@@ -675,7 +690,7 @@ cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
 size_t verify_scratch_bytes(int batch, int total, int vocab) {
   const size_t sc = scan_chunks<uint32_t>(vocab), pc = pick_chunks(vocab, kFew);  // the more of them
   return align16((size_t)(total + batch) * sc * sizeof(float2)) +
-         align16((size_t)(total + batch) * sizeof(float)) + align16((size_t)total) +
+         2 * align16((size_t)(total + batch) * sizeof(float)) + align16((size_t)total) +
          align16((size_t)batch * sizeof(Draw)) + (size_t)batch * 2 * pc * sizeof(Part) +
          (size_t)batch * pc * sizeof(double);
 }
@@ -707,6 +722,8 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   s += align16((size_t)(a.total + a.batch) * sc * sizeof(float2));
   p.ref = reinterpret_cast<float*>(s);
   s += align16((size_t)(a.total + a.batch) * sizeof(float));
+  p.owner = reinterpret_cast<int*>(s);
+  s += align16((size_t)(a.total + a.batch) * sizeof(int));
   p.state = s;
   s += align16((size_t)a.total);
   p.draw = reinterpret_cast<Draw*>(s);

@@ -643,10 +643,11 @@ DD_API dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch
  *                  sequence b's k_b + 1 rows start at cu_draft[b] + b
  *   draft_logits   [total, vocab], draft_stride elements between rows
  *   draft_tokens   int32 [total];  draft_conf fp32 [total]
- *   cu_draft       device int32 [B + 1]; a row outside [0, total] or
- *                  decreasing, like a token outside the vocabulary, latches
- *                  DD_ERR_DEVICE_BOUNDS (the row gets accepted = 0 and no
- *                  tokens; the token is refused)
+ *   cu_draft       device int32 [B + 1]; a row outside [0, total], or
+ *                  decreasing, or that starts before the end of a row before
+ *                  it that is neither, like a token outside the vocabulary,
+ *                  latches DD_ERR_DEVICE_BOUNDS (the row gets accepted = 0 and
+ *                  no tokens, the token is refused; the other rows stand)
  *   u_accept       fp32 [total];  u_sample fp32 [B]
  *   accepted       int32 [B]: n_b
  *   tokens         int32 [total + B]: from cu_draft[b] + b on, the n_b

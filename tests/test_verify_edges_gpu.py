@@ -7,7 +7,9 @@ import numpy as np
 import pytest
 import torch
 
-from test_verify_gpu import _case, _check, _run
+import block_discrete_diffusion_dd_b200 as dd
+import paged_ref as ref
+from test_verify_gpu import DEV, _case, _check, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +75,67 @@ def test_verify_decides_tiny_probabilities_exactly(tau, off):
     assert case["draft_conf"].item() == conf
     o = _run(case, float(np.float32(tau)), 1.0)
     assert o["accepted"].tolist() == [1 if off > 0 else 0]
+
+
+def _standing(cu, most):
+    """The rows that stand: possible by themselves and behind those before."""
+    end, rows = 0, []
+    for q0, q1 in zip(cu[:-1], cu[1:]):
+        rows.append(end <= q0 <= q1 <= most)
+        end = q1 if rows[-1] else end
+    return rows
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("cu", [
+    [0, 9, 5, 8],        # a row past the end: the last one stands all the same
+    [0, 8, 3, 6],        # a row inside the first one
+    [-4, 2, 5, 8],
+    [0, 3, -7, 8],
+    [0, BIG, -BIG - 1, 8],
+    [2, 2, 4, 8, 1, 8],
+    [8, 0, 8, 8],
+    [2, 4, 4, 7],        # in order; packed rows of no sequence
+])
+@pytest.mark.parametrize("before,V", [(0, 700), (300, 50)])
+def test_verify_offsets_out_of_order_leave_the_standing_rows(cu, before, V):
+    cu = list(range(before)) + [before + x if abs(x) < 1000 else x for x in cu]
+    T, B = before + 8, len(cu) - 1
+    stands = _standing(cu, T)
+    c, tau, tau_d = _case((T,) + (0,) * (B - 1), V, torch.float32, 51, noise=0.5)
+    c["cu_draft"] = torch.tensor(cu, dtype=torch.int32)
+    # each row that stands alone, as a batch of its own
+    out = dict(accepted=torch.zeros(B, dtype=torch.int32),
+               tokens=torch.full((T + B,), 77, dtype=torch.int32),
+               target_prob=torch.full((T,), 77.0, dtype=torch.float64))
+    for b in range(B):
+        if stands[b]:
+            d, t = slice(cu[b], cu[b + 1]), slice(cu[b] + b, cu[b + 1] + b + 1)
+            out["accepted"][b:b + 1], out["tokens"][t], out["target_prob"][d] = ref.verify(
+                c["target_logits"][t], c["draft_logits"][d], c["draft_tokens"][d],
+                c["draft_conf"][d], [0, cu[b + 1] - cu[b]], c["u_accept"][d],
+                c["u_sample"][b:b + 1], tau, tau_d)
+    # states that an earlier call has left: every draft refused, then all accepted
+    ws = dd.new_workspace(dd.verify_draft_workspace_bytes(B, T, V))
+    dev = {k: v.to(DEV) for k, v in c.items()}
+    for u in (1e30, 0.0):
+        dd.verify_draft(**dict(dev, cu_draft=torch.tensor([0] + [T] * B, dtype=torch.int32, device=DEV),
+                               u_accept=torch.full((T,), u, device=DEV)), workspace=ws)
+        o = dd.verify_draft_outputs(B, T, DEV)
+        for x in o.values():
+            x.fill_(77)
+        dd.verify_draft(**dev, outputs=o, workspace=ws)
+        if all(stands):
+            dd.query_device_error(ws)
+        else:
+            with pytest.raises(dd.DDError) as err:
+                dd.query_device_error(ws)
+            assert err.value.status == 6  # DD_ERR_DEVICE_BOUNDS
+        assert torch.equal(o["accepted"].cpu(), out["accepted"])
+        assert torch.equal(o["tokens"].cpu(), out["tokens"])
+        mine = out["target_prob"] != 77
+        got = o["target_prob"].cpu().double()
+        assert ((got - out["target_prob"]).abs()[mine] <= 2e-6 * out["target_prob"][mine]).all()
+        assert (got[~mine] == 77).all()
