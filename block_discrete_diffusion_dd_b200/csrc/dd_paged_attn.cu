@@ -41,8 +41,14 @@
 //            cache stands for.  The scale bytes follow the page by cp.async.
 // The tensor core runs one thread's MMAs in issue order.  Where P takes S's
 // place with two query tiles, S_q(j) complete therefore means PV_q(j-1)
-// complete, and O may be rescaled; elsewhere a rescale waits for PV(j-1) on
-// its own barrier.
+// complete, and O may be rescaled; elsewhere a rescale waits for PV(j-1) on a
+// barrier of the P.V products.  A wait tells a phase from its neighbours only
+// by parity, so that when it starts, the product before the awaited one on the
+// same barrier has to be known complete, and the one behind it not to be
+// possible.  The latter needs P of this warp.  The former holds with a barrier
+// per query tile where S(j) complete means PV(j-1) complete, or where every
+// tile waits for the P.V product before it (kSep); one query tile, where S(j)
+// complete means PV(j-2) complete, takes two barriers in turn.
 //
 // What bounds it (D = 128, 148 CTAs): with 256 query rows the softmax, whose
 // 16 warps take about 1.4 us per key tile (loads and maximum 0.3, row
@@ -261,8 +267,9 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
     };
     // P.V product t of this query tile is complete
     auto wait_pv = [&](int t) {
+      const int bar = kQT == 1 ? t & 1 : q, phase = kQT == 1 ? t >> 1 : t;
       const bool done = __all_sync(
-          0xffffffffu, mbar_wait_bounded(&bars->pv_done[q], t & 1, abort_flag, p.wait_ns));
+          0xffffffffu, mbar_wait_bounded(&bars->pv_done[bar], phase & 1, abort_flag, p.wait_ns));
       tc_fence_after();
       return done;
     };
@@ -450,9 +457,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
       }
       if (!ok) break;
       // epilogue: O / l and the log-sum-exp
-      // (a wait tells a phase from the one before it only, so the last but one
-      // comes first where nothing else has waited for it)
-      if (((kQT == 1 || L::kSep) && cnt > 1 && !wait_pv(cnt - 2)) || !wait_pv(cnt - 1)) {
+      if (!wait_pv(cnt - 1)) {
         ok = false;
         break;
       }
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(Lay<D, kF8, kQT>::kThreads, 1)
             const uint32_t aP = L::kSep ? L::kTmemP + q * (BN / 2) : buf * BN;
             if (leader) issue_pv<D>(tmem + L::kTmemO + q * D, tmem + aP, bv, j > 0);
             __syncwarp();
-            commit(&bars->pv_done[q]);
+            commit(&bars->pv_done[buf]);  // (one query tile: two in turn, as P's buffers)
             // P in the place of S: the next S has to come behind its P.V
             if (!L::kSep && kQT == 2 && j + 1 < n) ok = s_of(q, j + 1);
           }

@@ -201,3 +201,28 @@ def test_prefixes_out_of_order_leave_the_standing_rows(cu, kind):
             if n:
                 want[cu[b]:cu[b] + n] = ref.sequence(pool, pr, b, n).transpose(0, 1)
         assert torch.equal(out.double().cpu(), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,new", [(64, 30), (128, 30), (64, 90), (128, 90)])
+def test_attention_many_items_of_few_key_tiles(kind, D, new):
+    # items of one to six key tiles, several to a CTA and some split between two,
+    # with one query tile and with two: every call gives the same result
+    H, B = 8, 30
+    g = torch.Generator().manual_seed(D + new)
+    past = torch.randint(0, 640, (B,), generator=g).tolist()
+    pr = ref.problem((new,) * B, past, 16, seed=2)
+    k, v = (_normal((pr.pages, H, 16, D), i) for i in (1, 2))
+    cache, k64, v64 = _quantised_cache(k, v)
+    if kind == "bf16":
+        cache, k64, v64 = dd.PagedCache(k.to(DEV), v.to(DEV)), k.double(), v.double()
+    q = _normal((new * B, 2 * H, D), 3)
+    # (a wide spread of scores: references move along the keys)
+    first = _check_attn(q, cache, k64, v64, pr, scale=0.6)
+    batch = dd.PagedBatch(pr.page_table.to(DEV), pr.cu_new.to(DEV), pr.kv_len.to(DEV), new)
+    ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, new * B, 2 * H))
+    dev = q.to(DEV)
+    for _ in range(20):
+        out, _ = dd.paged_attn(dev, cache, batch, scale=0.6, workspace=ws)
+        assert torch.equal(out, first)
+    dd.query_device_error(ws)
