@@ -188,10 +188,14 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool narrow = p.b.batch <= 32;  // one warp's work
   if (!narrow || warp == 0) {
-  bool order = true;  // every row's offsets are possible by themselves
-  for (int b = threadIdx.x; b < p.b.batch; b += kT)
-    order = offsets_fit(p.b.cu_new, b, p.b.total_new) && order;
-  order = narrow ? __all_sync(0xffffffffu, order) : __syncthreads_and(order);
+  // every row's offsets are possible by themselves (a round of rows that is the
+  // only one finds that out as it is weighed)
+  bool order = true;
+  if (p.b.batch > kT) {
+    for (int b = threadIdx.x; b < p.b.batch; b += kT)
+      order = offsets_fit(p.b.cu_new, b, p.b.total_new) && order;
+    order = __syncthreads_and(order);
+  }
   bool many = false;  // an item of more than kMost tiles (one barrier serves this too)
   int item = 0;       // units of an item of this thread's sequence
   // exclusive prefix of v over the block; *all gets the block's sum
@@ -225,11 +229,15 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
   auto weigh = [&](int b0) {
     const int b = b0 + threadIdx.x;
     w = 0;
+    if (b < p.b.batch) r = chunk_row(p.b, b, 0, p.err);
+    if (p.b.batch <= kT) {
+      const bool fits = b >= p.b.batch || offsets_fit(p.b.cu_new, b, p.b.total_new);
+      order = narrow ? __all_sync(0xffffffffu, fits) : __syncthreads_and(fits);
+    }
     if (b < p.b.batch) {
-      int end = 0;  // of the rows before
-      for (int a = order ? b : 0; a <= b; ++a) {
-        r = chunk_row(p.b, a, end, p.err);
-        end = r.q0 + r.n;
+      if (!order) {
+        r = ChunkRow{0, 0, 0};
+        for (int a = 0; a <= b; ++a) r = chunk_row(p.b, a, r.q0 + r.n, p.err);
       }
       w = row_weight<kRows, kFixed>(p, r);
       many = w > kMost + kFixed;
