@@ -895,8 +895,7 @@ size_t paged_attn_scratch_bytes(const PagedAttnArgs& a) {
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   const bool f8 = a.pool.e4m3;
   const int D = a.p.head_dim;
-  const int64_t rows = max_rows(a);
-  if (rows == 0) return cudaSuccess;
+  const int64_t rows = max_rows(a);  // (none: the lengths are checked all the same)
   const int sms = num_sms();
   Params p{};
   p.b = a.p;

@@ -226,3 +226,26 @@ def test_attention_many_items_of_few_key_tiles(kind, D, new):
         out, _ = dd.paged_attn(dev, cache, batch, scale=0.6, workspace=ws)
         assert torch.equal(out, first)
     dd.query_device_error(ws)
+
+
+def test_rows_above_a_bound_of_none_are_latched():
+    # max_new = 0 with new tokens: impossible rows, for append and attention alike
+    H, D = 2, 64
+    pr = ref.problem((2, 0, 1), (9, 5, 30), 8)
+    cache = dd.new_paged_cache(pr.pages, 8, H, D)
+    x = _normal((3, 2 * H, D), 1).to(DEV)
+    batch = dd.PagedBatch(pr.page_table.to(DEV), pr.cu_new.to(DEV), pr.kv_len.to(DEV), 0)
+    ws = dd.new_workspace(dd.paged_attn_workspace_bytes(cache, batch, 3, 2 * H))
+    dd.cache_append(cache, batch, x[:, :H], x[:, H:], workspace=ws)
+    _latched(ws, True)
+    assert (cache.k == 0).all() and (cache.v == 0).all()
+    out = torch.full((3, 2 * H, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((3, 2 * H), 7.0, device=DEV)
+    dd.paged_attn(x, cache, batch, out=out, lse=lse, workspace=ws)
+    _latched(ws, True)
+    assert (out == 7).all() and (lse == 7).all()
+    # no new tokens at all: nothing wrong with that bound
+    none = dd.PagedBatch(batch.page_table, torch.zeros_like(batch.cu_new), batch.kv_len, 0)
+    dd.paged_attn(x, cache, none, out=out, lse=lse, workspace=ws)
+    _latched(ws, False)
+    assert (out == 7).all() and (lse == 7).all()
