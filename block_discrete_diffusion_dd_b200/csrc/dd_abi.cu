@@ -1299,8 +1299,15 @@ dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch* batch
 
 static constexpr int kMaxDraftVocab = 1 << 30;  // (entry indices, and a chunk past the last)
 
+// Rows of one call times chunks of a row, which a grid and its indices cover.
+static bool draft_rows_fit(int batch, int total, int vocab) {
+  return ((int64_t)total + batch) * (((int64_t)vocab + 2047) / 2048) <= INT32_MAX;
+}
+
 size_t dd_verify_draft_workspace(int batch, int total, int vocab) {
-  if (batch < 0 || total < 0 || vocab < 1 || vocab > kMaxDraftVocab) return 0;
+  if (batch < 0 || total < 0 || vocab < 1 || vocab > kMaxDraftVocab ||
+      !draft_rows_fit(batch, total, vocab))
+    return 0;
   return kPagedHeader + verify_scratch_bytes(batch, total, vocab);
 }
 
@@ -1325,7 +1332,7 @@ dd_status dd_verify_draft(const dd_verify_params* params, dd_dtype dtype, int ba
     if (!std::isfinite(t) || t < 1e-3f)
       return fail(DD_ERR_INVALID_ARG, "temperatures must be finite and >= 1e-3");
   if (vocab > kMaxDraftVocab) return fail(DD_ERR_UNSUPPORTED, "vocab=%d exceeds 2^30", vocab);
-  if (((int64_t)total + batch) * (((int64_t)vocab + 2047) / 2048) > INT32_MAX)
+  if (!draft_rows_fit(batch, total, vocab))
     return fail(DD_ERR_UNSUPPORTED, "rows * chunks exceeds 2^31");
   if (batch == 0) return DD_OK;
   if (!target_logits || !cu_draft || !u_sample || !accepted || !tokens)

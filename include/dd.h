@@ -654,7 +654,8 @@ DD_API dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch
  *                  accepted tokens, the next token, and -1
  *   target_prob    fp32 [total]: p_i(x_i)
  *   workspace      >= dd_verify_draft_workspace(...) bytes, 256-byte
- *                  aligned (0 from the query on invalid arguments) */
+ *                  aligned (0 from the query on arguments that are invalid or
+ *                  too large) */
 typedef struct {
   float temperature, draft_temperature;
 } dd_verify_params;
