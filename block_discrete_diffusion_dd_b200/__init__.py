@@ -716,6 +716,8 @@ def _own(workspace: torch.Tensor, device):
     if workspace.device != device or workspace.dtype != torch.uint8:
         raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected "
                          f"torch.uint8 on {device}")
+    if not workspace.is_contiguous():  # (its size is counted by elements)
+        raise ValueError("workspace must be contiguous")
 
 
 def _packed(t: torch.Tensor, heads: int, dim: int, dtype, device, what: str) -> int:

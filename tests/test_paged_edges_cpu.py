@@ -1,6 +1,7 @@
 """Sizes at the ends of what the paged and verification calls take (no GPU:
 nothing is launched)."""
 import pytest
+import torch
 
 import block_discrete_diffusion_dd_b200 as dd
 from block_discrete_diffusion_dd_b200 import build as libbuild
@@ -26,3 +27,13 @@ def test_verify_workspace_of_the_largest_calls(batch, total, vocab, fits):
     n = dd.verify_draft_workspace_bytes(batch, total, vocab)
     rows, chunks = batch + total, -(-vocab // 4096)
     assert (n >= 8 * rows * chunks) if fits else n == 0
+
+
+def test_workspaces_whose_elements_overlap_are_refused():
+    cpu = torch.device("cpu")
+    ws = torch.zeros(512, dtype=torch.uint8)
+    dd._own(ws, cpu)
+    dd._own(ws[256:], cpu)
+    for bad in (ws[:1].expand(4096), ws[::2], ws.int()):
+        with pytest.raises(ValueError):
+            dd._own(bad, cpu)
