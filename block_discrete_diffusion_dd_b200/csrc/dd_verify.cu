@@ -219,11 +219,10 @@ __global__ void __launch_bounds__(kThreads, kScanBlocks)
   const int blocks = (p.vocab + skew + kE - 1) / kE;
   const bool whole = (p.vocab + skew) % kE == 0;  // the last block is all the row's
   const int chunk0 = seg * per;
-  // (asked before the logits are, needed after them)
-  bool order = true;
-#pragma unroll 1
-  for (int b = threadIdx.x; b < p.batch; b += kThreads)
-    order = offsets_fit(p.cu, b, p.total) && order;
+  // whether the offsets are in order: asked before the logits are and needed
+  // after them, or (large batches) asked by the rows' last CTAs alone
+  const bool large = p.batch > kThreads;
+  bool order = large || (int)threadIdx.x >= p.batch || offsets_fit(p.cu, threadIdx.x, p.total);
   auto load = [&](int ch, uint4 (&v)[kBlocks]) {
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
@@ -300,6 +299,12 @@ __global__ void __launch_bounds__(kThreads, kScanBlocks)
   }
   order = __syncthreads_and(order);
   if (!last) return;
+  if (large) {
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.batch; b += kThreads)
+      order = offsets_fit(p.cu, b, p.total) && order;
+    order = __syncthreads_and(order);
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = cls + warp * (int)kPagedCounters; r < rows; r += kThreads / 32 * (int)kPagedCounters) {
     // the sequence whose rows cu[b] + b .. cu[b + 1] + b hold r: by bisection,
