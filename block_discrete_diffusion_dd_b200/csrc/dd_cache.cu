@@ -37,7 +37,7 @@ namespace dd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 4;  // CTAs per SM (64 registers)
+constexpr int kBlocks = 4;  // CTAs of the append per SM (64 registers; 73 took 118 us for 110)
 
 // Largest |x| of the 8 bf16 values in v, as bf16 bits (which order like the
 // magnitudes they stand for; 0x7f80 and above are infinities and NaN).
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 }
 
 template <int D, bool kF8, int N>
-__global__ void __launch_bounds__(kThreads, kBlocks)
+__global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const PagedBatch p, const void* k_pool, const void* v_pool,
                       const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
                       uint4* __restrict__ k_out, uint4* __restrict__ v_out, uint32_t* err) {
