@@ -124,6 +124,7 @@ template <typename R, typename F>
 __device__ __forceinline__ bool place_tokens(int64_t* rows, int first, int count,
                                              const PagedBatch& p, int most, R&& row, F&& of) {
   bool order = true;
+#pragma unroll 1
   for (int b = (int)((threadIdx.x + kThreads - 32) % kThreads); b < p.batch; b += kThreads) {
     order = offsets_fit(p.cu_new, b, most) && order;
     if (blockIdx.x == 0) row(b, 0);
@@ -145,6 +146,7 @@ __device__ __forceinline__ void place_in_turn(int64_t* rows, int first, int coun
     const int t = first + k;
     rows[k] = -1;
     ChunkRow c{0, 0, 0};
+#pragma unroll 1
     for (int b = 0; b < p.batch && t < p.total_new; ++b) {
       c = row(b, c.q0 + c.n);
       if (t >= c.q0 && t - c.q0 < c.n) rows[k] = of(t, b, c);

@@ -237,6 +237,7 @@ __device__ void find_share(const Params& p, Share* sh, int64_t* warp_sums) {
     if (b < p.b.batch) {
       if (!order) {
         r = ChunkRow{0, 0, 0};
+#pragma unroll 1
         for (int a = 0; a <= b; ++a) r = chunk_row(p.b, a, r.q0 + r.n, p.err);
       }
       w = row_weight<kRows, kFixed>(p, r);
