@@ -24,11 +24,12 @@
 // head); D / 8 lanes move it, 16 bytes of bf16 each.  A CTA takes N units per
 // lane group, all of their loads in flight at once, and looks its few tokens'
 // places up once, in shared memory; appending, the loads do not wait for that.
-// Measured, 8 kv heads of 128: an E4M3 append of 76,588 tokens 101 us, 4.7 TB/s,
-// with instructions issued in 71% of the cycles (largest magnitude, scale and
-// codes of every row); 81,986 tokens of a bf16 cache read in 104 us, the rate
-// of a copy; 4,096 tokens of an E4M3 cache read in 5.8 us; one token of 32
-// sequences appended in 2.7 us.
+// Measured, 8 kv heads of 128 (replayed from a graph): an E4M3 append of 76,588
+// tokens 103 us, 4.6 TB/s, with instructions issued in 73% of the cycles
+// (largest magnitude, scale and codes of every row), a bf16 one 97 us, the rate
+// of a copy; 81,986 tokens of a bf16 cache read in 104 us, the rate of a copy,
+// of an E4M3 cache in 94 (5.4 TB/s); 4,096 tokens of an E4M3 cache in 5.9 us; one
+// token of 32 sequences appended in 2.5 us.
 #include <climits>
 
 #include "dd_paged.cuh"

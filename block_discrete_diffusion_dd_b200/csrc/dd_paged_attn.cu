@@ -54,14 +54,15 @@
 // 16 warps take about 1.4 us per key tile (loads and maximum 0.3, row
 // reductions 0.3, exponentials 0.7, stores 0.1) and wait 0.3 us for the tensor
 // core, against 1.0 us of tensor-core work: two chunks of 2,048 tokens over
-// 8,192 take 225 us, or 260 once the power limit holds the clock down (the
+// 8,192 take 232 us, or 257 once the power limit holds the clock down (the
 // products alone: 135), the tensor pipe being active half of the time.  With
 // an E4M3 cache the conversion: 1.0 us for K and 0.9 us for V of a tile (blocks
-// of 256 tokens of eight sequences with up to 16,384 each: 135 us, from bf16
-// 117).  A short past is bounded by the
+// of 256 tokens of eight sequences with up to 16,384 each: 136 us, from bf16
+// 117; the two chunks 275, or 290).  (The registers are spent too: with two
+// query tiles 96 a thread, or 80, and the kernels spill up to 40 bytes.)  A short past is bounded by the
 // chain of single steps: the share's search 2.3 us, the Q tile 2.4, the first
 // product 0.8, the epilogue 2.6, and the second kernel 5 to 8 (one block of
-// 256 over 4,096: 27 us).
+// 256 over 4,096: 28.3 us).
 //
 // What the cache holds past a sequence's length may be anything, NaN
 // included: masked scores are replaced before they are used, and V rows past
@@ -884,14 +885,18 @@ size_t paged_attn_scratch_bytes(const PagedAttnArgs& a) {
 
 // Up to kFewRows query rows per sequence and kv head, the kernel for few rows
 // (dd_paged_few.cu).  Measured against the tensor-core kernel, D = 128, groups
-// of two, 64 sequences of up to 16,384 tokens: E4M3, one token each 195 us
-// against 421, eight tokens (16 rows) 306 against 421; bf16 316 against 377 and
-// 350 against 404.  One sequence of 65,536: bf16 50 against 58 us (16 rows: 58
-// against 65), E4M3 36 against 65 (55 against 69).
+// of two, 64 sequences of up to 16,384 tokens: E4M3, one token each 194 us
+// against 423, eight tokens (16 rows) 325 against 426; bf16 317 against 397 and
+// 346 against 414.  One sequence of 65,536: bf16 52 against 58 us (16 rows: 56
+// against 62), E4M3 37 against 67 (58 against 70).
 // Above that and up to one tile of rows the tensor-core kernel with one query
-// tile: eight sequences, 32 and 128 rows, bf16 47 and 50 us against 51 and 54
-// with the other, E4M3 54 and 59 against 61 and 67.  More rows: two query
+// tile: eight sequences, 32 and 128 rows, bf16 48 and 51 us against 52 and 55
+// with the other, E4M3 55 and 60 against 60 and 67.  More rows: two query
 // tiles, so that a key tile is fetched (and expanded) once for 256 rows.
+// (The host knows the bound max_new, not the lengths: in a batch of single tokens
+// and one chunk, or under a loose bound, the single tokens take the kernel of the
+// longest.  63 of them beside a chunk of 2,048 tokens: E4M3 630 us, bf16 503, of
+// which the single tokens alone, with their own bound, would be 180 and 296.)
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
   const bool f8 = a.pool.e4m3;
   const int D = a.p.head_dim;

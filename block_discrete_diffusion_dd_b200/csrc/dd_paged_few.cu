@@ -41,12 +41,13 @@
 // row that puts its largest magnitude in [2^14, 2^15); only what lies 2^28
 // below it loses bits.
 //
-// Measured (D = 128, one token per sequence, group of two): 64 sequences of up
-// to 16,384 tokens, bf16 316 us (6.6 TB/s, the rate of a copy), E4M3 195 us
-// (5.4 TB/s; expanding the codes and the softmax take the issue slots 42% of
-// the time); one sequence of 65,536, bf16 50 us (5.4 TB/s: about 8 us of it are
-// start, merge and end).  Two short sequences at D = 64 take 6.9 us, all of it
-// latency: the launch, the lengths, the key tiles one after the other.
+// Measured (D = 128, one token per sequence, group of two; replayed from a
+// graph): 64 sequences of up to 16,384 tokens, bf16 317 us (6.6 TB/s, the rate of
+// a copy), E4M3 194 us (5.5 TB/s; 204 to 208 with other inputs each time;
+// expanding the codes and the softmax take the issue slots 43% of the time); one
+// sequence of 65,536, bf16 52 us (5.2 TB/s: about 8 us of it are start, merge and
+// end).  Two short sequences at D = 64 take 7.1 us, all of it latency: the
+// launch, the lengths, the key tiles one after the other.
 #include "dd_paged_attn.cuh"
 
 namespace dd {
@@ -70,9 +71,9 @@ struct Few {
   static constexpr int kBlocks = kSmall ? kFewBlocks : 1;
   static constexpr int kRows = 8 * NT;
   // key tiles of an item that a CTA takes whole where there are CTAs enough:
-  // two sequences of up to 700 tokens (D = 64) 6.9 us against 8.2 shared out; 16
-  // of 512 at D = 128 9.1 against 13.9, of 1,024 13.5 against 18.9 (E4M3: 512
-  // 10.8 against 11.9, but 1,024 16.1 against 14.8)
+  // two sequences of up to 700 tokens (D = 64) 7.1 us against 8.4 shared out; 16
+  // of 512 at D = 128 9.3 against 14.0, of 1,024 13.5 against 18.9 (E4M3: 512
+  // 11.3 against 12.7, 768 14.0 against 14.6, but 1,024 16.6 against 15.5)
   static constexpr int kMostWhole = kF8 ? 6 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kLd = D + 4;  // floats per row of the merge area

@@ -434,9 +434,6 @@ int sm_count_se() {
 
 }  // namespace
 
-// 2-D bf16 map over [outer, inner] with a row stride in elements, box
-// (box_inner, box_outer), box_inner * 2 bytes of swizzling (64 or 128),
-// zero fill out of bounds.
 bool encode_3d(CUtensorMap* m, const void* base, bool bytes, const int64_t (&dims)[3],
                const int64_t (&strides)[2], const int (&box)[3], bool swizzle128) {
   EncodeTiledFn fn = encode_fn();
@@ -451,6 +448,9 @@ bool encode_3d(CUtensorMap* m, const void* base, bool bytes, const int64_t (&dim
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D bf16 map over [outer, inner] with a row stride in elements, box
+// (box_inner, box_outer), box_inner * 2 bytes of swizzling (64 or 128),
+// zero fill out of bounds.
 bool encode_2d(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t stride,
                int box_inner, int box_outer) {
   EncodeTiledFn fn = encode_fn();

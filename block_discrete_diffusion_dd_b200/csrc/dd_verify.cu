@@ -40,10 +40,10 @@
 // phase is one or two barriers.  Sums are taken in a fixed order, so a call's
 // result does not depend on scheduling.
 //
-// Measured, bf16, 262,144 entries: eight sequences with 358 drafted tokens 64
-// us, of which the scan 39 (4.9 TB/s; instructions issued in 60% of the
-// cycles) and norm and pick 25; one sequence with eight drafted tokens 17.9
-// us, nearly all of it the chain of the three kernels.
+// Measured, bf16, 262,144 entries: eight sequences with 358 drafted tokens 65.5
+// us (fp32 89), of which the scan 40 (4.8 TB/s; instructions issued in 59% of
+// the cycles) and norm and pick 25; one sequence with eight drafted tokens 18.5
+// us (fp32 20.3), nearly all of it the chain of the three kernels.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -681,9 +681,9 @@ cudaError_t launch_verify_t(const VerifyParams& p, cudaStream_t stream) {
   };
   // Few chunks (one per SM at most) are waited for, each thread's entries one
   // after the other: with half as many bf16 entries per thread one sequence of
-  // 262,144 takes 17.9 us (19.5), of 32,000 15.6 (18.3).  Many chunks cost by
-  // their number: eight sequences take 63.8 us with 8 entries, 66.9 with 4 (and
-  // fp32 rows, whose 8 are two loads, 19.6 and 20.4).
+  // 262,144 takes 18.5 us (20.1), of 32,000 16.3 (19.1).  Many chunks cost by
+  // their number: eight sequences take 65.5 us with 8 entries, 68.8 with 4 (and
+  // one of fp32 rows, whose 8 are two loads, 20.3 and 20.9).
   if constexpr (sizeof(T) == 2)
     if ((int64_t)p.batch * pick_chunks(p.vocab, kMany) <= 148)
       return draw(std::integral_constant<int, kFew>{});

@@ -562,7 +562,8 @@ DD_API size_t dd_cache_workspace(void);
  *                 v_stride elements between tokens (>= heads_kv * head_dim,
  *                 a multiple of 8): views of a fused projection are taken
  *   workspace     >= dd_cache_workspace() bytes, 256-byte aligned
- * total_new * 2 * heads_kv <= 2^30 (as in dd_cache_read).  A DD_BF16 cache takes the bits as they are.  A DD_E4M3 cache takes, per
+ * total_new * 2 * heads_kv <= 2^30 (as in dd_cache_read).
+ * A DD_BF16 cache takes the bits as they are.  A DD_E4M3 cache takes, per
  * (token, head), with a the largest finite magnitude of its head_dim values,
  * the scale 2^e of the least integer e with a <= 448 * 2^e (within
  * [-120, 120]; 0 when a = 0) and the codes E4M3(x * 2^-e), rounded to
