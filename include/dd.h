@@ -583,7 +583,7 @@ DD_API dd_status dd_cache_append(const dd_paged_cache* cache, const dd_paged_bat
  *   cu_prefix     device int32 [batch + 1]; a sequence is taken as empty
  *                 (which latches DD_ERR_DEVICE_BOUNDS) unless 0 <=
  *                 cu_prefix[b] <= cu_prefix[b+1] and it starts at or behind
- *                 the end of every one before it that is not
+ *                 the end of every earlier sequence that is possible so
  *   total         rows of the outputs; rows of no sequence are left as they
  *                 were, and so are rows whose position or page does not exist
  *                 (which latch DD_ERR_DEVICE_BOUNDS); the prefixes may go on
@@ -644,11 +644,11 @@ DD_API dd_status dd_paged_attn(const dd_paged_cache* cache, const dd_paged_batch
  *                  sequence b's k_b + 1 rows start at cu_draft[b] + b
  *   draft_logits   [total, vocab], draft_stride elements between rows
  *   draft_tokens   int32 [total];  draft_conf fp32 [total]
- *   cu_draft       device int32 [B + 1]; a row outside [0, total], or
- *                  decreasing, or that starts before the end of a row before
- *                  it that is neither, like a token outside the vocabulary,
- *                  latches DD_ERR_DEVICE_BOUNDS (the row gets accepted = 0 and
- *                  no tokens, the token is refused; the other rows stand)
+ *   cu_draft       device int32 [B + 1]; a row that leaves [0, total],
+ *                  decreases or starts before the end of an earlier row that
+ *                  stands latches DD_ERR_DEVICE_BOUNDS and gets accepted = 0
+ *                  and no tokens (the other rows stand); a token outside the
+ *                  vocabulary latches it too and is refused
  *   u_accept       fp32 [total];  u_sample fp32 [B]
  *   accepted       int32 [B]: n_b
  *   tokens         int32 [total + B]: from cu_draft[b] + b on, the n_b
