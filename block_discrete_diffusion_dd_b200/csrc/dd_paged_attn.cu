@@ -50,19 +50,19 @@
 // tile waits for the P.V product before it (kSep); one query tile, where S(j)
 // complete means PV(j-2) complete, takes two barriers in turn.
 //
-// What bounds it (D = 128, 148 CTAs): with 256 query rows the softmax, whose
-// 16 warps take about 1.4 us per key tile (loads and maximum 0.3, row
-// reductions 0.3, exponentials 0.7, stores 0.1) and wait 0.3 us for the tensor
-// core, against 1.0 us of tensor-core work: two chunks of 2,048 tokens over
-// 8,192 take 232 us, or 257 once the power limit holds the clock down (the
-// products alone: 135), the tensor pipe being active half of the time.  With
-// an E4M3 cache the conversion: 1.0 us for K and 0.9 us for V of a tile (blocks
-// of 256 tokens of eight sequences with up to 16,384 each: 136 us, from bf16
-// 117; the two chunks 275, or 290).  (The registers are spent too: with two
-// query tiles 96 a thread, or 80, and the kernels spill up to 40 bytes.)  A short past is bounded by the
-// chain of single steps: the share's search 2.3 us, the Q tile 2.4, the first
-// product 0.8, the epilogue 2.6, and the second kernel 5 to 8 (one block of
-// 256 over 4,096: 28.3 us).
+// What bounds it (D = 128, 148 CTAs): with 256 query rows the softmax, whose 16
+// warps take about 1.4 us per key tile (loads and maximum 0.3, row reductions
+// 0.3, exponentials 0.7, stores 0.1) and wait 0.3 us for the tensor core,
+// against 1.0 us of tensor-core work: two chunks of 2,048 tokens over 8,192
+// take 232 us, or 257 once the power limit holds the clock down (the products
+// alone: 135), the tensor pipe being active half of the time.  With an E4M3
+// cache the conversion: 1.0 us for K and 0.9 us for V of a tile (blocks of 256
+// tokens of eight sequences with up to 16,384 each: 136 us, from bf16 117; the
+// two chunks 275, or 290).  (The registers are spent too: with two query tiles
+// 96 a thread, or 80, and the kernels spill up to 40 bytes.)  A short past is
+// bounded by the chain of single steps: the share's search 2.3 us, the Q tile
+// 2.4, the first product 0.8, the epilogue 2.6, and the second kernel 5 to 8
+// (one block of 256 over 4,096: 28.3 us).
 //
 // What the cache holds past a sequence's length may be anything, NaN
 // included: masked scores are replaced before they are used, and V rows past
